@@ -113,7 +113,9 @@ def _new_counts(case):
 
 def _e4m3(x):
     """e4m3 codes of x with one factor per last-dimension vector."""
-    f = x.abs().amax(-1).clamp_min(1e-30) / E4M3_MAX
+    # The factor is divided out in 64 bits (the rounded quotient is fp32's): a CUDA tensor over a
+    # constant is a product with the constant's rounded reciprocal, which moves codes next to a border.
+    f = (x.abs().amax(-1).clamp_min(1e-30).double() / E4M3_MAX).float()
     return (x / f[..., None]).to(torch.float8_e4m3fn).view(torch.uint8), f
 
 
