@@ -36,7 +36,7 @@ def sources():
 
 
 def deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "fa.h")]
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, h) for h in ("fa.h", "fa_cache.h")]
 
 
 def needs_build() -> bool:

@@ -12,6 +12,7 @@
 
 #include "fa.h"
 #include "fa_bwd.cuh"
+#include "fa_cache.h"
 #include "fa_dq.cuh"
 #include "fa_fwd.cuh"
 
@@ -428,7 +429,7 @@ static int bwd_common(const void *q, const void *k, const void *v, const void *o
 
 extern "C" {
 
-int fa_version(void) { return 300; }  // 0.3.0: fa_fwd_fp8, the no-alloc status reader
+int fa_version(void) { return 400; }  // 0.4.0: the paged cache (fa_cache.h)
 
 const char *fa_status_string(int status) {
   switch (status) {
@@ -441,6 +442,7 @@ const char *fa_status_string(int status) {
     case FA_ERR_CUDA: return "FA_ERR_CUDA: CUDA call or launch failed";
     case FA_ERR_DEVICE_TIMEOUT: return "FA_ERR_DEVICE_TIMEOUT: a kernel gave up on a pipeline wait";
     case FA_ERR_DEVICE_INTERNAL: return "FA_ERR_DEVICE_INTERNAL: kernel launch environment unusable";
+    case FA_ERR_DEVICE_CACHE: return "FA_ERR_DEVICE_CACHE: a page id or a sequence length was out of range";
     default: return "unknown fa_status";
   }
 }
@@ -540,12 +542,13 @@ int fa_device_status_info(void *stream, int *info) {
     info[0] = h[1];
     info[1] = h[2];
     info[2] = h[3];
-    info[3] = h[4];
+    info[3] = h[0] == FA_ERR_DEVICE_CACHE ? h[5] : h[4];
   }
   if (cudaMemset(ds->status, 0, kStatusInts * sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
+  if (h[0] == FA_ERR_DEVICE_CACHE) return FA_ERR_DEVICE_CACHE;
   return h[0] == fa::kStatusInternal ? FA_ERR_DEVICE_INTERNAL : FA_ERR_DEVICE_TIMEOUT;
 }
 
@@ -693,3 +696,6 @@ extern "C" int fa_noalloc_selftest_timeout(void *stream) {
   fa_selftest_timeout_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(ns->status, next_seq());
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
+
+// The entry points of fa_cache.h, on the services above.
+#include "fa_cache_api.cuh"

@@ -1,0 +1,213 @@
+// fa_cache_api.cuh -- the C ABI of the paged key/value cache (declared in
+// include/fa_cache.h): argument validation and the launches of the append, gather
+// and decode kernels.  Part of fa_api.cu, whose device state and checks it uses.
+#pragma once
+
+#include "fa_cache.cuh"
+#include "fa_cache.h"
+#include "fa_decode.cuh"
+
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// One of K and V: a stride matters only along an axis of more than one element,
+// where it holds at least a row and keeps every row 16-byte aligned.
+int check_strides(const long long *stride, const int *extent, int d, int elem_bytes) {
+  for (int a = 0; a < 3; ++a) {
+    if (extent[a] == 1) continue;
+    if (stride[a] < d || stride[a] >= (1ll << 39)) return FA_ERR_UNSUPPORTED;
+    if (stride[a] * elem_bytes % 16 != 0) return FA_ERR_MISALIGNED;
+  }
+  return FA_OK;
+}
+
+// Checks of the cache that all entry points share (no CUDA calls).
+int check_cache(const fa_paged_cache *c) {
+  if (!c || !c->k || !c->v || !c->block_table || !c->seq_lens) return FA_ERR_INVALID_ARG;
+  if (c->type != FA_CACHE_BF16 && c->type != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
+  if (c->type == FA_CACHE_E4M3 && (!c->k_scale || !c->v_scale)) return FA_ERR_INVALID_ARG;
+  if (c->B < 1 || c->H < 1 || c->num_pages < 1 || c->max_pages < 1 || c->page_size < 1) return FA_ERR_INVALID_ARG;
+  if (c->block_table_stride < c->max_pages && c->B > 1) return FA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+  const int ps = c->page_size;
+  if (ps != 16 && ps != 32 && ps != 64 && ps % 128 != 0) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->max_pages) * ps >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->block_table) || !aligned4(c->seq_lens))
+    return FA_ERR_MISALIGNED;
+  const int extent[3] = {c->num_pages, c->H, ps};
+  const int eb = c->type == FA_CACHE_BF16 ? 2 : 1;
+  int st = check_strides(c->k_stride, extent, c->d, eb);
+  if (st == FA_OK) st = check_strides(c->v_stride, extent, c->d, eb);
+  if (st != FA_OK) return st;
+  if (c->type == FA_CACHE_E4M3) {
+    if (!aligned4(c->k_scale) || !aligned4(c->v_scale)) return FA_ERR_MISALIGNED;
+    for (int a = 0; a < 3; ++a)
+      if (extent[a] > 1 && (c->k_scale_stride[a] < 1 || c->v_scale_stride[a] < 1 ||
+                            c->k_scale_stride[a] >= (1ll << 39) || c->v_scale_stride[a] >= (1ll << 39)))
+        return FA_ERR_UNSUPPORTED;
+  }
+  return FA_OK;
+}
+
+int make_view(const fa_paged_cache *c, fa::CacheView *v, DeviceState **ds) {
+  const int st = device_state(ds, nullptr);
+  if (st != FA_OK) return st;
+  v->kv[0] = static_cast<uint8_t *>(c->k);
+  v->kv[1] = static_cast<uint8_t *>(c->v);
+  v->scale[0] = c->k_scale;
+  v->scale[1] = c->v_scale;
+  for (int a = 0; a < 3; ++a) {
+    v->stride[0][a] = c->k_stride[a];
+    v->stride[1][a] = c->v_stride[a];
+    v->scale_stride[0][a] = c->k_scale_stride[a];
+    v->scale_stride[1][a] = c->v_scale_stride[a];
+  }
+  v->block_table = c->block_table;
+  v->seq_lens = c->seq_lens;
+  v->bt_stride = c->block_table_stride;
+  v->num_pages = c->num_pages;
+  v->H = c->H;
+  v->page_size = c->page_size;
+  v->B = c->B;
+  v->max_pages = c->max_pages;
+  v->page_shift = -1;
+  for (int s = 4; s < 31; ++s)
+    if (c->page_size == (1 << s)) v->page_shift = s;
+  v->status = (*ds)->status;
+  v->seq = next_seq();
+  return FA_OK;
+}
+
+// Blocks of kCacheThreads for n threads, or 0 if there are more than a grid holds.
+unsigned blocks_for(long long n) {
+  const long long g = (n + fa::kCacheThreads - 1) / fa::kCacheThreads;
+  return g > 0x7fffffffll ? 0u : static_cast<unsigned>(g);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_cache_append(const fa_paged_cache *cache, const void *k_new, const void *v_new, const long long *k_new_stride,
+                    const long long *v_new_stride, int T, const int *cu_new, void *stream) {
+  int st = check_cache(cache);
+  if (st != FA_OK) return st;
+  if (!k_new_stride || !v_new_stride || T < 0) return FA_ERR_INVALID_ARG;
+  if (!cu_new && T != cache->B) return FA_ERR_INVALID_ARG;
+  if (T == 0) return FA_OK;
+  if (!k_new || !v_new) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(cu_new)) return FA_ERR_MISALIGNED;
+  const long long *strides[2] = {k_new_stride, v_new_stride};
+  const int extent[2] = {T, cache->H};
+  fa::AppendParams p;
+  for (int w = 0; w < 2; ++w)
+    for (int a = 0; a < 2; ++a) {
+      const long long s = strides[w][a];
+      if (extent[a] > 1 && (s < 0 || s >= (1ll << 39))) return FA_ERR_UNSUPPORTED;
+      if (extent[a] > 1 && s % 8 != 0) return FA_ERR_MISALIGNED;
+      p.x_stride[w][a] = s;
+    }
+  DeviceState *ds = nullptr;
+  st = make_view(cache, &p.c, &ds);
+  if (st != FA_OK) return st;
+  p.x[0] = static_cast<const uint16_t *>(k_new);
+  p.x[1] = static_cast<const uint16_t *>(v_new);
+  p.cu_new = cu_new;
+  p.T = T;
+  const unsigned grid = blocks_for(2ll * T * cache->H * (cache->d / 8));
+  if (grid == 0) return FA_ERR_UNSUPPORTED;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->type == FA_CACHE_E4M3;
+  if (cache->d == 64) {
+    if (e4m3)
+      fa::fa_cache_append_kernel<64, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
+    else
+      fa::fa_cache_append_kernel<64, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
+  } else {
+    if (e4m3)
+      fa::fa_cache_append_kernel<128, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
+    else
+      fa::fa_cache_append_kernel<128, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_cache_gather(const fa_paged_cache *cache, void *k_out, void *v_out, int rep, int N, void *stream) {
+  int st = check_cache(cache);
+  if (st != FA_OK) return st;
+  if ((!k_out && !v_out) || rep < 1 || N < 1) return FA_ERR_INVALID_ARG;
+  const long double elems = static_cast<long double>(cache->B) * cache->H * rep * N * cache->d;
+  if (elems >= 2147483648.0L) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(k_out) || !aligned16(v_out)) return FA_ERR_MISALIGNED;
+  fa::GatherParams p;
+  DeviceState *ds = nullptr;
+  st = make_view(cache, &p.c, &ds);
+  if (st != FA_OK) return st;
+  p.out[0] = static_cast<uint16_t *>(k_out);
+  p.out[1] = static_cast<uint16_t *>(v_out);
+  p.rep = rep;
+  p.N = N;
+  const dim3 grid(blocks_for(static_cast<long long>(cache->B) * cache->H * N * (cache->d / 8)), 2);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->type == FA_CACHE_E4M3;
+  if (cache->d == 64) {
+    if (e4m3)
+      fa::fa_cache_gather_kernel<64, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
+    else
+      fa::fa_cache_gather_kernel<64, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
+  } else {
+    if (e4m3)
+      fa::fa_cache_gather_kernel<128, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
+    else
+      fa::fa_cache_gather_kernel<128, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_decode_workspace_bytes(int B, int Hq, int H, int d) {
+  if (B < 1 || H < 1 || Hq < H || Hq % H != 0 || (d != 64 && d != 128)) return 0;
+  return 256;
+}
+
+int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, int Hq, float scale, int window,
+              void *workspace, size_t workspace_bytes, void *stream) {
+  int st = check_cache(cache);
+  if (st != FA_OK) return st;
+  if (!q || !o || Hq < 1 || Hq % cache->H != 0 || window < 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(cache->B) * Hq * cache->d >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(o) || !aligned4(lse)) return FA_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < fa_decode_workspace_bytes(cache->B, Hq, cache->H, cache->d))
+    return FA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FA_ERR_MISALIGNED;
+  if (cache->B > 65535) return FA_ERR_UNSUPPORTED;
+  fa::DecodeParams p;
+  DeviceState *ds = nullptr;
+  st = make_view(cache, &p.c, &ds);
+  if (st != FA_OK) return st;
+  p.q = static_cast<const uint16_t *>(q);
+  p.o = static_cast<uint16_t *>(o);
+  p.lse = lse;
+  p.Hq = Hq;
+  p.G = Hq / cache->H;
+  p.window = window;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const dim3 grid(Hq, cache->B);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache->type == FA_CACHE_E4M3;
+  if (cache->d == 64) {
+    if (e4m3)
+      fa::fa_decode_kernel<64, true><<<grid, fa::kDecodeThreads, 0, s>>>(p);
+    else
+      fa::fa_decode_kernel<64, false><<<grid, fa::kDecodeThreads, 0, s>>>(p);
+  } else {
+    if (e4m3)
+      fa::fa_decode_kernel<128, true><<<grid, fa::kDecodeThreads, 0, s>>>(p);
+    else
+      fa::fa_decode_kernel<128, false><<<grid, fa::kDecodeThreads, 0, s>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,511 @@
+"""GPU tests of the paged key/value cache: append, gather and decode against their
+definitions in 64 bits, at the lengths, layouts and sharings where they can go
+wrong, and as they are used together."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from cache_helpers import BF16_HALF, DEV, Cache, check_decode, decode_exact
+from io_aware_exact_23_b200 import binding as fa
+
+pytestmark = pytest.mark.gpu
+
+EDGES = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 300, 1000]
+
+
+def ok():
+    st, info = fa.fa_device_status(info=True)
+    assert st == 0, f"device status {st} {info}"
+
+
+def make_q(B, Hq, d, seed=0, mult=1.0):
+    g = torch.Generator(device="cpu").manual_seed(seed + 77)
+    return (torch.randn(B, Hq, d, generator=g) * mult).to(torch.bfloat16).to(DEV)
+
+
+def decode(c, q, scale=None, window=0, lse=True, ws=None, stream=None, out=None):
+    B, Hq, d = q.shape
+    o = torch.full_like(q, float("nan")) if out is None else out
+    L = torch.full((B, Hq), float("nan"), device=DEV) if lse else None
+    if ws is None:
+        ws = torch.full((fa.fa_decode_workspace_bytes(B, Hq, c.H, d),), 0xFF, dtype=torch.uint8, device=DEV)
+    fa.fa_decode(q, c.k, c.v, o=o, lse=L, scale=scale or 1 / math.sqrt(d), workspace=ws, window=window, stream=stream,
+                 **c.args)
+    return o, L
+
+
+def run_decode(c, q, label="", **kw):
+    o, L = decode(c, q, **kw)
+    ok()
+    w = kw.get("window", 0)
+    check_decode(o, L, decode_exact(c, q, kw.get("scale") or 1 / math.sqrt(q.shape[2]), w), label)
+    return o, L
+
+
+# ------------------------------------------------------------------- decode
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 64, 128, 256])
+def test_decode_lengths(d, page, e4m3):
+    c = Cache(EDGES, 2, d, page, e4m3, "nhd" if page == 16 else "hnd", seed=page)
+    run_decode(c, make_q(c.B, 8, d))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 7, 8, 9, 12, 16, 17, 24, 31, 32, 33, 40, 64, 71])
+def test_decode_shared_heads(G, e4m3):
+    d = 128 if G % 2 else 64
+    c = Cache([5, 0, 200, 513], 2, d, 32, e4m3, seed=G)
+    run_decode(c, make_q(c.B, 2 * G, d, seed=G))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "joint", "padded"])
+@pytest.mark.parametrize("page", [16, 32, 384])
+def test_decode_layouts(layout, page, e4m3):
+    for d in (64, 128):
+        c = Cache([130, 7, 900], 3, d, page, e4m3, layout, seed=3)
+        run_decode(c, make_q(c.B, 6, d), f"{layout} {page} {d}")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window", [1, 2, 100, 127, 128, 129, 500, 5000])
+def test_decode_window(window, e4m3):
+    c = Cache([0, 1, 128, 129, 300, 1025], 2, 128 if window % 2 else 64, 16, e4m3, seed=window)
+    run_decode(c, make_q(c.B, 8, c.d), window=window)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_large_logits(d, e4m3):
+    """Nearly one-hot rows whose maximum keeps moving: the running maximum has to rescale."""
+    c = Cache([700, 1, 2049], 2, d, 64, e4m3, seed=5, mult=8.0)
+    run_decode(c, make_q(c.B, 8, d, mult=8.0))
+    # Scores that climb by 20 from each token to the next, and that fall.
+    for sign in (1.0, -1.0):
+        c = Cache([400], 1, d, 16, e4m3, seed=6)
+        q = torch.zeros(1, 4, d, device=DEV, dtype=torch.bfloat16)
+        q[:, :, 0] = 1
+        r = torch.zeros(400, 1, d, device=DEV, dtype=torch.bfloat16)
+        r[:, 0, 0] = torch.arange(400, device=DEV) * 20 * sign
+        c.put(c.k, c.ks, 0, torch.arange(400, device=DEV), r)
+        run_decode(c, q, scale=1.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_e4m3_factors_of_every_size(d):
+    """Factors that differ by 2^40 from row to row, and rows of zeros."""
+    c = Cache([600, 37], 2, d, 16, True, seed=8)
+    g = torch.Generator(device="cpu").manual_seed(1)
+    for b, n in enumerate((600, 37)):
+        pos = torch.arange(n, device=DEV)
+        f = torch.exp2(torch.randint(-20, 20, (n, 1, 1), generator=g).float()).to(DEV)
+        r = torch.randn(n, 2, d, generator=g).to(DEV) * f
+        r[::7] = 0
+        c.put(c.v, c.vs, b, pos, r.to(torch.bfloat16))
+    run_decode(c, make_q(2, 8, d))
+
+
+def test_decode_sink_and_many_small():
+    """One key far above many others whose weights only count together."""
+    for e4m3 in (False, True):
+        n = 20000
+        c = Cache([n], 1, 64, 64, e4m3, seed=9, mult=0.05)
+        r = torch.zeros(1, 1, 64, device=DEV, dtype=torch.bfloat16)
+        r[0, 0, :] = 1
+        c.put(c.k, c.ks, 0, torch.zeros(1, dtype=torch.long, device=DEV), r)
+        q = torch.ones(1, 8, 64, device=DEV, dtype=torch.bfloat16)
+        run_decode(c, q, scale=9.0 / 64)  # the sink's score is 9: about as much weight as the rest
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_many_sequences_and_few_tiles(e4m3):
+    """More sequences than threads of a block, and grids with fewer tiles than SMs."""
+    r = torch.Generator(device="cpu").manual_seed(4)
+    lens = torch.randint(0, 40, (700,), generator=r).tolist()
+    lens[100:400] = [0] * 300
+    c = Cache(lens, 1, 64, 16, e4m3, seed=10)
+    run_decode(c, make_q(700, 2, 64))
+    for n in (1, 129, 3000, 18944, 19000):
+        c = Cache([n], 1, 128, 128, e4m3, seed=n)
+        run_decode(c, make_q(1, 5, 128), f"n = {n}")
+
+
+def test_decode_all_idle():
+    c = Cache([0, 0, 0], 2, 64, 16, False)
+    o, L = run_decode(c, make_q(3, 4, 64))
+    assert (o == 0).all() and (L == -math.inf).all()
+
+
+def test_decode_without_lse_and_odd_scale():
+    c = Cache([77, 300], 2, 128, 32, False, seed=12)
+    run_decode(c, make_q(2, 8, 128), lse=False, scale=0.37)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_repeats_bit_for_bit_wherever_the_pages_lie(e4m3):
+    lens = [3000, 17, 0, 900, 128]
+    a, b = (Cache(lens, 4, 128, 16, e4m3, seed=20) for _ in range(2))
+    b.table.copy_(torch.where(b.table >= 0, b.num - 1 - b.table, b.table))
+    b.k, b.v = a.k.flip(0), a.v.flip(0)
+    if e4m3:
+        b.ks, b.vs = a.ks.flip(0), a.vs.flip(0)
+    q = make_q(5, 16, 128)
+    o, L = run_decode(a, q)
+    for c in (a, a, b):
+        o2, L2 = decode(c, q)
+        assert torch.equal(o, o2) and torch.equal(L, L2)
+    ok()
+
+
+def test_decode_shared_prefix():
+    """Two sequences whose tables name the same pages."""
+    c = Cache([256, 256], 2, 64, 64, False, seed=21)
+    c.table[1] = c.table[0]
+    q = make_q(1, 4, 64).expand(2, -1, -1).contiguous()
+    o, L = run_decode(c, q)
+    assert torch.equal(o[0], o[1])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_offsets_beyond_32_bits(e4m3):
+    """Pages that start more than 2^32 elements into the cache."""
+    dt = torch.uint8 if e4m3 else torch.bfloat16
+    page, d = 128, 128
+    P = (1 << 32) // (page * d) + 40
+    big = torch.empty((P, 1, page, d), dtype=dt, device=DEV)
+    c = Cache([200, 300], 1, d, page, e4m3, seed=22)
+    at = P - c.num
+    big[at:] = c.k
+    c.k = big
+    vbig = torch.empty((P, 1, page, d), dtype=dt, device=DEV)
+    vbig[at:] = c.v
+    c.v = vbig
+    if e4m3:
+        pad = torch.full((at, 1, page), float("nan"), device=DEV)
+        c.ks, c.vs = torch.cat([pad, c.ks]), torch.cat([pad, c.vs])
+    c.table.copy_(torch.where(c.table >= 0, c.table + at, c.table))
+    run_decode(c, make_q(2, 4, d))
+    new = torch.randn(2, 1, d, device=DEV).to(torch.bfloat16)
+    fa.fa_cache_append(new, new, c.k, c.v, **c.args)
+    out = torch.empty(2, 1, 300, d, dtype=torch.bfloat16, device=DEV)
+    fa.fa_cache_gather(c.k, c.v, k_out=out, v_out=None, **c.args)
+    ok()
+    if not e4m3:
+        assert torch.equal(out[0, 0, 199], new[0, 0]) and torch.equal(out[1, 0, 299], new[1, 0])
+    ref = c.rows("k", 1, 300)[0]
+    assert ((out[1, 0].double() - ref).abs() <= BF16_HALF * ref.abs()).all()
+
+
+def test_decode_on_another_stream_and_two_at_once():
+    c = Cache([5000, 300], 2, 128, 64, False, seed=23)
+    c2 = Cache([4000, 900, 2], 2, 64, 64, True, seed=24)
+    q, q2 = make_q(2, 8, 128), make_q(3, 8, 64)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append((decode(c, q, stream=s1), decode(c2, q2, stream=s2)))
+        torch.cuda.synchronize()
+    ok()
+    for a, b in got:
+        check_decode(*a, decode_exact(c, q, 1 / math.sqrt(128)))
+        check_decode(*b, decode_exact(c2, q2, 1 / math.sqrt(64)))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_in_a_graph_follows_its_inputs(e4m3):
+    """A captured step replayed with other lengths, tables, keys and queries."""
+    c = Cache([700] * 4, 2, 128, 16, e4m3, seed=25)  # every row that a step may read is written
+    q = make_q(4, 8, 128)
+    new = torch.randn(2, 4, 2, 128, device=DEV).to(torch.bfloat16)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(4, 8, 2, 128), dtype=torch.uint8, device=DEV)
+    o, L = decode(c, q, ws=ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):  # two graphs that share the workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fa.fa_cache_append(new[0], new[1], c.k, c.v, **c.args)
+            fa.fa_decode(q, c.k, c.v, o=o, lse=L, scale=0.1, workspace=ws, **c.args)
+        graphs.append(g)
+    for step, lens in enumerate(([700, 400, 128, 33], [1, 0, 300, 600], [0, 0, 0, 0], [650, 1, 17, 700])):
+        c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.copy_(make_q(4, 8, 128, seed=step))
+        new.normal_()
+        o.fill_(float("nan"))
+        graphs[step % 2].replay()
+        ok()
+        check_decode(o, L, decode_exact(c, q, 0.1), f"step {step}")
+
+
+def test_decode_nan_stays_in_its_sequence():
+    """A NaN in a visible row reaches that sequence's heads and no other's."""
+    c = Cache([300, 300, 40], 2, 64, 16, False, seed=26)
+    page, off = c.where(1, torch.tensor([150], device=DEV))
+    c.v[page[0], 0, off[0]] = float("nan")
+    q = make_q(3, 4, 64)
+    o, _ = decode(c, q)
+    ok()
+    assert torch.isnan(o[1, :2]).all() and torch.isfinite(o[1, 2:]).all()
+    assert torch.isfinite(o[0]).all() and torch.isfinite(o[2]).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("what", ["page", "negative page", "length", "negative length"])
+def test_bad_tables_are_reported(what, e4m3):
+    """A page id or length out of range is recorded, never followed, and leaves the others' rows right."""
+    c = Cache([200, 200, 90], 2, 64, 16, e4m3, seed=27)
+    q = make_q(3, 4, 64)
+    ref = decode_exact(c, q, 1 / 8)
+    if what.endswith("page"):
+        c.table[1, 3] = c.num if what == "page" else -1
+    else:
+        c.lens[1] = 16 * c.per + 1 if what == "length" else -3
+    if what == "length":
+        c.table[1] = c.table[0, 0]  # every page the clamped length reaches is a valid one
+    o, L = decode(c, q)
+    st, info = fa.fa_device_status(info=True)
+    assert st == 9 and info[:2] == [8, 1], (st, info)
+    assert fa.fa_device_status() == 0
+    keep = torch.tensor([0, 2], device=DEV)
+    check_decode(o[keep], L[keep], tuple(x[keep] for x in ref))
+    new = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=DEV)
+    if what.endswith("length"):
+        fa.fa_cache_append(new, new, c.k, c.v, **c.args)
+        assert fa.fa_device_status(info=True)[1][:2] == [6, 1]
+    out = torch.empty(3, 2, 200, 64, dtype=torch.bfloat16, device=DEV)
+    fa.fa_cache_gather(c.k, c.v, k_out=out, v_out=None, **c.args)
+    st, info = fa.fa_device_status(info=True)
+    assert st == 9 and info[:2] == [7, 1]
+
+
+# ------------------------------------------------------------------- append
+def append_reference(c, k_new, v_new, counts):
+    """The cache's tensors after the append, from the definition (a copy)."""
+    want = [x if x is None else x.clone() for x in (c.k, c.v, c.ks, c.vs)]
+    at = 0
+    for b, m in enumerate(counts):
+        n = int(c.lens[b])
+        pos = torch.arange(n - m, n, device=DEV)
+        keep = pos >= 0
+        for x, f, new in ((want[0], want[2], k_new), (want[1], want[3], v_new)):
+            if keep.any():
+                c.put(x, f, b, pos[keep], new[at:at + m][keep])
+        at += m
+    return want
+
+
+def same(a, b):
+    if a is None:
+        return b is None
+    if a.dtype == torch.uint8:  # codes stand for values: both NaN codes are one
+        a, b = a.view(torch.float8_e4m3fn).float(), b.view(torch.float8_e4m3fn).float()
+    return torch.equal(torch.nan_to_num(a.float(), nan=12345.0), torch.nan_to_num(b.float(), nan=12345.0))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "joint", "padded"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_one_token(d, layout, e4m3):
+    c = Cache([1, 0, 16, 17, 128, 129, 40], 3, d, 16, e4m3, layout, seed=30)
+    qkv = torch.randn(7, 5, 3, d, device=DEV).to(torch.bfloat16)  # K and V sliced out of wider rows
+    k, v = qkv[:, 1], qkv[:, 3]
+    want = append_reference(c, k, v, [1] * 7)
+    fa.fa_cache_append(k, v, c.k, c.v, **c.args)
+    ok()
+    for got, w in zip((c.k, c.v, c.ks, c.vs), want):
+        assert same(got, w)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [16, 128])
+def test_append_prompts(page, e4m3):
+    """Whole prompts, parts, none, more tokens than the sequence holds, and padding behind the last."""
+    lens, counts = [300, 5, 0, 128, 40, 1], [300, 2, 0, 128, 45, 0]
+    c = Cache(lens, 2, 128, page, e4m3, "nhd", seed=31)
+    T = sum(counts)
+    new = torch.randn(2, T + 9, 2, 128, device=DEV).to(torch.bfloat16)
+    want = append_reference(c, new[0], new[1], counts)
+    cu = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device=DEV)
+    fa.fa_cache_append(new[0], new[1], c.k, c.v, cu_new=cu, **c.args)
+    ok()
+    for got, w in zip((c.k, c.v, c.ks, c.vs), want):
+        assert same(got, w)
+
+
+def test_append_many_sequences():
+    counts = [(i * 7) % 5 for i in range(600)]
+    c = Cache([n + 3 for n in counts], 1, 64, 16, True, seed=32)
+    new = torch.randn(2, sum(counts), 1, 64, device=DEV).to(torch.bfloat16)
+    want = append_reference(c, new[0], new[1], counts)
+    cu = torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32, device=DEV)
+    fa.fa_cache_append(new[0], new[1], c.k, c.v, cu_new=cu, **c.args)
+    ok()
+    for got, w in zip((c.k, c.v, c.ks, c.vs), want):
+        assert same(got, w)
+
+
+def test_append_of_hard_values():
+    """Zeros, subnormals, the largest numbers, ties, infinities and NaN."""
+    d = 64
+    c = Cache([1] * 7, 1, d, 16, True, seed=33)
+    x = torch.randn(7, 1, d, device=DEV).to(torch.bfloat16)
+    x[0] = 0
+    x[1] *= 1e-38
+    x[2] *= 1e38
+    x[3] = torch.arange(d, device=DEV).to(torch.bfloat16) * 7  # 441 = 448 - 7: codes between which ties fall
+    x[3, 0, 0] = 448
+    x[4, 0, 5] = float("inf")
+    x[5, 0, 9] = float("nan")
+    x[6] *= 1e-30
+    want = append_reference(c, x, x, [1] * 7)
+    fa.fa_cache_append(x, x, c.k, c.v, **c.args)
+    ok()
+    for got, w in zip((c.k, c.v, c.ks, c.vs), want):
+        assert same(got, w)
+
+
+def test_append_of_nothing():
+    c = Cache([3, 4], 1, 64, 16, False)
+    z = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device=DEV)
+    cu = torch.zeros(3, dtype=torch.int32, device=DEV)
+    before = c.k.clone()
+    fa.fa_cache_append(z, z, c.k, c.v, cu_new=cu, **c.args)
+    ok()
+    assert same(before, c.k)
+
+
+# ------------------------------------------------------------------- gather
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "joint", "padded"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rep,N", [(1, 1), (3, 130), (4, 700)])
+def test_gather(d, layout, e4m3, rep, N):
+    lens = [1, 0, 64, 129, 513]
+    c = Cache(lens, 2, d, 64 if d == 64 else 16, e4m3, layout, seed=40)
+    out = [torch.full((5, 2 * rep, N, d), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    fa.fa_cache_gather(c.k, c.v, k_out=out[0], v_out=out[1], **c.args)
+    ok()
+    for nm, got in zip("kv", out):
+        want = torch.zeros(5, 2, N, d, dtype=torch.float64, device=DEV)
+        for b, n in enumerate(lens):
+            m = min(n, N)
+            if m:
+                want[b, :, :m] = c.rows(nm, b, m)
+        want = want.repeat_interleave(rep, 1)
+        if e4m3:  # code * factor in fp32, then bf16: two roundings
+            assert ((got.double() - want).abs() <= (BF16_HALF + 2.0 ** -23) * want.abs()).all()
+        else:
+            assert torch.equal(got.double(), want)
+
+
+def test_gather_one_of_two():
+    c = Cache([70], 2, 64, 16, False, seed=41)
+    a, b = (torch.full((1, 2, 70, 64), 3.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    fa.fa_cache_gather(c.k, c.v, k_out=a, v_out=None, **c.args)
+    fa.fa_cache_gather(c.k, c.v, k_out=None, v_out=b, **c.args)
+    ok()
+    assert torch.equal(a.double()[0], c.rows("k", 0, 70)) and torch.equal(b.double()[0], c.rows("v", 0, 70))
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_then_tokens(d, e4m3):
+    """As a server runs them: fa_fwd over the prompts, one append of their keys and
+    values, then tokens one at a time; and the cache read back into fa_fwd."""
+    prompts, steps, H, G, page = [150, 31, 128], 20, 2, 4, 16
+    ends = [n + steps for n in prompts]
+    c = Cache(ends, H, d, page, e4m3, seed=50, fill=False)
+    N = max(ends)
+    g = torch.Generator(device="cpu").manual_seed(51)
+    q, k, v = (torch.randn(3, h, N, d, generator=g).to(torch.bfloat16).to(DEV) for h in (H * G, H, H))
+    c.lens.copy_(torch.tensor(prompts, dtype=torch.int32))
+    pk = torch.cat([k[b, :, :n].transpose(0, 1) for b, n in enumerate(prompts)])
+    pv = torch.cat([v[b, :, :n].transpose(0, 1) for b, n in enumerate(prompts)])
+    cu = torch.tensor([0, 150, 181, 309], dtype=torch.int32, device=DEV)
+    fa.fa_cache_append(pk, pv, c.k, c.v, cu_new=cu, **c.args)
+    scale = 1 / math.sqrt(d)
+    got = []
+    for t in range(steps):
+        c.lens += 1
+        at = c.lens.long() - 1
+        b = torch.arange(3, device=DEV)
+        fa.fa_cache_append(k[b, :, at], v[b, :, at], c.k, c.v, **c.args)
+        o, L = decode(c, q[b, :, at].contiguous(), scale)
+        ref = decode_exact(c, q[b, :, at], scale)
+        check_decode(o, L, ref, f"step {t}")
+        got.append((at.tolist(), o, L))
+    ok()
+    # The whole sequences at once, from the cache: fa_fwd's causal rows are the steps' rows.
+    K, V = (torch.empty(3, H * G, N, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    fa.fa_cache_gather(c.k, c.v, k_out=K, v_out=V, **c.args)
+    o, lse = torch.empty_like(q), torch.empty(3, H * G, N, device=DEV)
+    fa.fa_fwd(q, K, V, o, lse, scale, True)
+    ok()
+    for at, od, Ld in got:
+        for b, n in enumerate(at):
+            # Both are within 1e-2 of exact attention (fa_fwd's gate; the read-back of e4m3
+            # rows rounds them to bf16 once more, 2^-9 of values below 5).
+            assert (o[b, :, n] - od[b]).abs().max() <= (4e-2 if e4m3 else 2e-2)
+            assert (lse[b, :, n] - Ld[b]).abs().max() <= (2e-2 if e4m3 else 2e-3)
+
+
+# ---------------------------------------------------------------- refusals
+def test_binding_refusals():
+    c = Cache([20, 30], 2, 64, 16, False)
+    e = Cache([20, 30], 2, 64, 16, True)
+    q = make_q(2, 4, 64)
+    o, L = torch.empty_like(q), torch.empty(2, 4, device=DEV)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(2, 4, 2, 64), dtype=torch.uint8, device=DEV)
+
+    def call(cc=c, **kw):
+        a = dict(q=q, k_cache=cc.k, v_cache=cc.v, o=o, lse=L, scale=0.1, workspace=ws, **cc.args)
+        a.update(kw)
+        fa.fa_decode(**a)
+
+    call()
+    call(e)
+    for bad in (dict(seq_lens=c.lens.long()), dict(q=q.float()), dict(v_cache=e.v), dict(lse=L.double()),
+                dict(workspace=None), dict(workspace=ws.float())):
+        with pytest.raises((TypeError, ValueError)):
+            call(**bad)
+    for bad in (dict(seq_lens=c.lens[:1]), dict(q=q[:1]), dict(o=o[:, :2]), dict(q=q.transpose(0, 1)), dict(lse=L[:1]),
+                dict(block_table=c.table[:1]), dict(block_table=c.table.t()), dict(v_cache=c.v[:1]),
+                dict(k_cache=c.k.transpose(2, 3), v_cache=c.v.transpose(2, 3)), dict(k_scale=e.ks),
+                dict(block_table=c.table.cpu()), dict(seq_lens=c.lens.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            call(**bad)
+    with pytest.raises((TypeError, ValueError)):
+        call(e, k_scale=None)
+    with pytest.raises((TypeError, ValueError)):
+        call(e, v_scale=e.vs[:1])
+    for bad, code in ((dict(workspace=ws[:16]), 4), (dict(scale=0.0), 1), (dict(window=-1), 1),
+                      (dict(q=make_q(2, 3, 64), o=torch.empty(2, 3, 64, dtype=torch.bfloat16, device=DEV), lse=None), 1)):
+        with pytest.raises(fa.FaError) as err:
+            call(**bad)
+        assert err.value.code == code
+    odd = torch.empty(c.num, 2, 16, 65, dtype=torch.bfloat16, device=DEV)[..., :64]  # rows off the 16-byte grid
+    with pytest.raises(fa.FaError) as err:
+        call(k_cache=odd, v_cache=odd)
+    assert err.value.code == 3
+    new = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    for bad in (dict(k_new=new[:1], v_new=new[:1]), dict(k_new=new.float()), dict(v_new=new[:, :1]),
+                dict(cu_new=torch.zeros(2, dtype=torch.int32, device=DEV)),
+                dict(cu_new=torch.zeros(3, dtype=torch.int64, device=DEV))):
+        a = dict(k_new=new, v_new=new, k_cache=c.k, v_cache=c.v, **c.args)
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            fa.fa_cache_append(**a)
+    out = torch.zeros(2, 4, 8, 64, dtype=torch.bfloat16, device=DEV)
+    for bad in (dict(k_out=None, v_out=None), dict(k_out=out[:, :3]), dict(k_out=out[:1]), dict(k_out=out.float()),
+                dict(k_out=out, v_out=out[:, :2]), dict(k_out=out.transpose(0, 1).contiguous().transpose(0, 1))):
+        a = dict(k_cache=c.k, v_cache=c.v, k_out=out, v_out=out, **c.args)
+        a.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            fa.fa_cache_gather(**a)
+    ok()
