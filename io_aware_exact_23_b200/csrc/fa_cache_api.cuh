@@ -85,6 +85,74 @@ unsigned blocks_for(long long n) {
   return g > 0x7fffffffll ? 0u : static_cast<unsigned>(g);
 }
 
+// K or V as the 4-D tensor (feature, row of the page, head, page) that the decode kernel
+// loads 128-byte (e4m3, d = 64: 64-byte) wide boxes of; pages past the last read as zeros.
+int encode_cache(CUtensorMap *m, const void *ptr, const fa_paged_cache *c, const long long *stride) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return FA_ERR_CUDA;
+  const int eb = c->type == FA_CACHE_BF16 ? 2 : 1;
+  const int row_bytes = c->d * eb, box_bytes = row_bytes < 128 ? row_bytes : 128;
+  // A stride along an axis of one element is never used, but has to be a valid one.
+  auto bytes = [&](int a, int extent) {
+    return static_cast<cuuint64_t>(extent > 1 ? stride[a] * eb : static_cast<long long>(row_bytes));
+  };
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->d), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->H), static_cast<cuuint64_t>(c->num_pages)};
+  const cuuint64_t strides[3] = {bytes(2, c->page_size), bytes(1, c->H), bytes(0, c->num_pages)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_bytes / eb),
+                             static_cast<cuuint32_t>(c->page_size < 128 ? c->page_size : 128), 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = enc(m, eb == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+                         const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// Query heads per block of the decode kernel: the smallest of its instances that holds G.
+int decode_block(int G) { return G <= 8 ? 8 : G <= 16 ? 16 : 32; }
+
+// Workspace: meta, then (m, l) and O of two parts per CTA.
+size_t decode_ml_offset() { return fa::kDecodeMaxCtas * sizeof(int4); }
+size_t decode_o_offset(int gb) { return decode_ml_offset() + 2ull * fa::kDecodeMaxCtas * gb * sizeof(float2); }
+size_t decode_bytes(int gb, int d) { return decode_o_offset(gb) + 2ull * fa::kDecodeMaxCtas * gb * d * sizeof(float); }
+
+template <int D, bool E4M3, int GB>
+cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p, unsigned grid,
+                          cudaStream_t stream) {
+  using C = fa::DecodeCfg<D, E4M3, GB>;
+  static std::atomic<unsigned long long> ready{0};  // devices whose kernel has its attribute
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!((ready.load() >> dev) & 1ull)) {
+    e = cudaFuncSetAttribute(fa::fa_decode_kernel<D, E4M3, GB>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << dev);
+  }
+  fa::fa_decode_kernel<D, E4M3, GB><<<grid, fa::kDecodeThreads, C::kSmemBytes, stream>>>(tk, tv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 1) return e;  // one CTA leaves no parts
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, static_cast<unsigned>(p.G < GB ? p.G : GB));
+  cfg.blockDim = dim3(fa::kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa::fa_decode_join_kernel<D, GB>, p);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_decode_block(int gb, const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p,
+                                unsigned grid, cudaStream_t s) {
+  return gb == 8    ? launch_decode<D, E4M3, 8>(tk, tv, p, grid, s)
+         : gb == 16 ? launch_decode<D, E4M3, 16>(tk, tv, p, grid, s)
+                    : launch_decode<D, E4M3, 32>(tk, tv, p, grid, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -167,7 +235,7 @@ int fa_cache_gather(const fa_paged_cache *cache, void *k_out, void *v_out, int r
 
 size_t fa_decode_workspace_bytes(int B, int Hq, int H, int d) {
   if (B < 1 || H < 1 || Hq < H || Hq % H != 0 || (d != 64 && d != 128)) return 0;
-  return 256;
+  return decode_bytes(decode_block(Hq / H), d);
 }
 
 int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, int Hq, float scale, int window,
@@ -181,7 +249,11 @@ int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, i
   if (!workspace || workspace_bytes < fa_decode_workspace_bytes(cache->B, Hq, cache->H, cache->d))
     return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_MISALIGNED;
-  if (cache->B > 65535) return FA_ERR_UNSUPPORTED;
+  // The kernel counts tiles of 128 positions, over all sequences and heads, in 31 bits.
+  const int G = Hq / cache->H, gb = decode_block(G), nblk = (G + gb - 1) / gb;
+  const long long item_tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 127) / 128;
+  const long double most = static_cast<long double>(cache->B) * cache->H * nblk * item_tiles;
+  if (most >= 2147483648.0L) return FA_ERR_UNSUPPORTED;
   fa::DecodeParams p;
   DeviceState *ds = nullptr;
   st = make_view(cache, &p.c, &ds);
@@ -190,24 +262,30 @@ int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, i
   p.o = static_cast<uint16_t *>(o);
   p.lse = lse;
   p.Hq = Hq;
-  p.G = Hq / cache->H;
+  p.G = G;
+  p.nblk = nblk;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid(Hq, cache->B);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.meta = reinterpret_cast<int4 *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(ws + decode_ml_offset());
+  p.part_o = reinterpret_cast<float *>(ws + decode_o_offset(gb));
+  CUtensorMap tk, tv;
+  if (encode_cache(&tk, cache->k, cache, cache->k_stride) || encode_cache(&tv, cache->v, cache, cache->v_stride))
+    return FA_ERR_CUDA;
+  // One CTA per SM (one fits), or one per tile if there can be no more.
+  unsigned grid = static_cast<unsigned>(ds->num_sms < fa::kDecodeMaxCtas ? ds->num_sms : fa::kDecodeMaxCtas);
+  if (most < static_cast<long double>(grid)) grid = static_cast<unsigned>(most);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == FA_CACHE_E4M3;
-  if (cache->d == 64) {
-    if (e4m3)
-      fa::fa_decode_kernel<64, true><<<grid, fa::kDecodeThreads, 0, s>>>(p);
-    else
-      fa::fa_decode_kernel<64, false><<<grid, fa::kDecodeThreads, 0, s>>>(p);
-  } else {
-    if (e4m3)
-      fa::fa_decode_kernel<128, true><<<grid, fa::kDecodeThreads, 0, s>>>(p);
-    else
-      fa::fa_decode_kernel<128, false><<<grid, fa::kDecodeThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  cudaError_t e;
+  if (cache->d == 64)
+    e = e4m3 ? launch_decode_block<64, true>(gb, tk, tv, p, grid, s) : launch_decode_block<64, false>(gb, tk, tv, p, grid, s);
+  else
+    e = e4m3 ? launch_decode_block<128, true>(gb, tk, tv, p, grid, s)
+             : launch_decode_block<128, false>(gb, tk, tv, p, grid, s);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"
