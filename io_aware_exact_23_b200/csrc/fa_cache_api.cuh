@@ -118,9 +118,13 @@ size_t decode_o_offset(int gb) { return decode_ml_offset() + 2ull * fa::kDecodeM
 size_t decode_bytes(int gb, int d) { return decode_o_offset(gb) + 2ull * fa::kDecodeMaxCtas * gb * d * sizeof(float); }
 
 template <int D, bool E4M3, int GB>
-cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p, unsigned grid,
-                          cudaStream_t stream) {
+cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p, int num_sms,
+                          long long most, cudaStream_t stream) {
   using C = fa::DecodeCfg<D, E4M3, GB>;
+  // As many CTAs as are resident at a time, or one per tile if there can be no more.
+  long long ctas = static_cast<long long>(num_sms) * C::kCtas;
+  if (ctas > fa::kDecodeMaxCtas) ctas = fa::kDecodeMaxCtas;
+  const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
   static std::atomic<unsigned long long> ready{0};  // devices whose kernel has its attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -130,7 +134,7 @@ cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev);
   }
-  fa::fa_decode_kernel<D, E4M3, GB><<<grid, fa::kDecodeThreads, C::kSmemBytes, stream>>>(tk, tv, p);
+  fa::fa_decode_kernel<D, E4M3, GB><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || grid == 1) return e;  // one CTA leaves no parts
   cudaLaunchConfig_t cfg = {};
@@ -147,10 +151,10 @@ cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa
 
 template <int D, bool E4M3>
 cudaError_t launch_decode_block(int gb, const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p,
-                                unsigned grid, cudaStream_t s) {
-  return gb == 8    ? launch_decode<D, E4M3, 8>(tk, tv, p, grid, s)
-         : gb == 16 ? launch_decode<D, E4M3, 16>(tk, tv, p, grid, s)
-                    : launch_decode<D, E4M3, 32>(tk, tv, p, grid, s);
+                                int num_sms, long long most, cudaStream_t s) {
+  return gb == 8    ? launch_decode<D, E4M3, 8>(tk, tv, p, num_sms, most, s)
+         : gb == 16 ? launch_decode<D, E4M3, 16>(tk, tv, p, num_sms, most, s)
+                    : launch_decode<D, E4M3, 32>(tk, tv, p, num_sms, most, s);
 }
 
 }  // namespace
@@ -273,17 +277,17 @@ int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, i
   CUtensorMap tk, tv;
   if (encode_cache(&tk, cache->k, cache, cache->k_stride) || encode_cache(&tv, cache->v, cache, cache->v_stride))
     return FA_ERR_CUDA;
-  // One CTA per SM (one fits), or one per tile if there can be no more.
-  unsigned grid = static_cast<unsigned>(ds->num_sms < fa::kDecodeMaxCtas ? ds->num_sms : fa::kDecodeMaxCtas);
-  if (most < static_cast<long double>(grid)) grid = static_cast<unsigned>(most);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == FA_CACHE_E4M3;
   cudaError_t e;
+  const int n = ds->num_sms;
+  const long long tiles = static_cast<long long>(most);
   if (cache->d == 64)
-    e = e4m3 ? launch_decode_block<64, true>(gb, tk, tv, p, grid, s) : launch_decode_block<64, false>(gb, tk, tv, p, grid, s);
+    e = e4m3 ? launch_decode_block<64, true>(gb, tk, tv, p, n, tiles, s)
+             : launch_decode_block<64, false>(gb, tk, tv, p, n, tiles, s);
   else
-    e = e4m3 ? launch_decode_block<128, true>(gb, tk, tv, p, grid, s)
-             : launch_decode_block<128, false>(gb, tk, tv, p, grid, s);
+    e = e4m3 ? launch_decode_block<128, true>(gb, tk, tv, p, n, tiles, s)
+             : launch_decode_block<128, false>(gb, tk, tv, p, n, tiles, s);
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

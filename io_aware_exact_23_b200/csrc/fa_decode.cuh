@@ -22,10 +22,16 @@
 // idle; the idle columns carry the low part of the operand that has to be rounded:
 // * bf16: P = hi + lo, both bf16 (16 significant bits), as 2 GB columns of O^T;
 // * e4m3: codes are multiplied as they are (kind::f8f6f4), the factor of K goes into the
-//   score, that of V into the weight.  q (8 bits, scaled by a power of two per head) is
-//   hi + lo / 16 in e4m3, exact to 2^-20 of the head's largest element; weights are
-//   hi + mid / 16 + lo / 256, 12 bits and not less than 2^-22 of the largest weight.
+//   score, that of V into the weight.  q (8 bits, scaled by one power of two per 8 heads) is
+//   hi + lo / 16 in e4m3, exact to 2^-20 of its largest element; weights, taken to fp16,
+//   are hi + mid / 16 + lo / 256: 11 bits, and not less than 2^-22 of the largest weight.
 // The columns' sums meet again in fp32.
+//
+// Softmax warps.  Four warps own the 128 keys of a tile for 8 query heads, GB / 8 such
+// groups per CTA.  P is the MN-major operand: a key's weights are adjacent bytes, so a
+// thread stores its 8 heads with two or three vector stores.  (With P K-major, one 2-byte
+// or 1-byte store per head and part, and all GB heads in one thread, a tile took 3000 to
+// 4000 cycles in e4m3; its share of the memory's rate allows 1430 at d = 128.)
 #pragma once
 
 #include <cstdint>
@@ -35,7 +41,7 @@
 
 namespace fa {
 
-constexpr int kDecodeMaxCtas = 192;  // workspace slots; the grid never exceeds it
+constexpr int kDecodeMaxCtas = 320;  // workspace slots; the grid never exceeds it
 
 struct DecodeParams {
   CacheView c;
@@ -59,41 +65,52 @@ struct DecodeCfg {
   static constexpr int kPanels = kRowBytes / kPanelRow;
   static constexpr int kPanelBytes = 128 * kPanelRow;
   static constexpr int kTileBytes = 128 * kRowBytes;
-  static constexpr int kQCols = E4M3 ? 2 * GB : (GB < 16 ? 16 : GB);
+  static constexpr int kGroups = GB / 8;                           // softmax warp groups
+  static constexpr int kQRows = E4M3 ? 2 * GB : GB;                // rows of Q in shared memory
+  static constexpr int kQCols = kQRows < 16 ? 16 : kQRows;         // columns of S^T
   static constexpr int kOParts = E4M3 ? 3 : 2;
-  static constexpr int kOCols = (kOParts * GB + 15) / 16 * 16;
-  static constexpr int kQBytes = kQCols * kRowBytes;
-  static constexpr int kPBytes = kOCols * 128 * kElem;
-  static constexpr int kScStages = 8;  // ring of the keys' factors (e4m3)
+  static constexpr int kOCols = (kOParts * GB + 15) / 16 * 16;     // columns of O^T
+  static constexpr int kPRow = E4M3 ? (GB == 8 ? 32 : GB == 16 ? 64 : 128) : 4 * GB;  // bytes of a key's row of P
+  static constexpr int kQBytes = kQRows * kRowBytes;
+  static constexpr int kPBytes = 128 * kPRow;
+  static constexpr int kScStages = 4;  // ring of the keys' factors (e4m3)
   // A score may exceed the running reference by kGrow (log2) before the reference moves;
   // e4m3 weights leave room for it below 448.
   static constexpr float kGrow = E4M3 ? 3.f : 8.f;
   static constexpr float kWeight = 32.f;  // e4m3: a weight of 1 is code value 32, 2^kGrow is 256
 
+  static constexpr int kSoftmaxWarps = 4 * kGroups;
+  static constexpr int kWarps = kSoftmaxWarps + 8;  // softmax, 4 epilogue, producer, issuer, Q, scales
+  static constexpr int kThreads = 32 * kWarps;
+  // Two CTAs per SM with 8 heads: one's tile hides the other's waits.
+  static constexpr int kCtas = GB == 8 ? 2 : 1;
+  static constexpr int kSmemMax = kCtas == 2 ? 115712 : 232448;
+
   static constexpr int kPOff = 0;
   static constexpr int kQOff = kPOff + 2 * kPBytes;
-  static constexpr int kScOff = kQOff + 2 * kQBytes;
-  static constexpr int kMiscOff = kScOff + (E4M3 ? kScStages * 1024 : 0);
-  // float: xmax[2][GB][4], lpart[2][4][GB], mref[2][GB], qscale[2][GB], vmax[2][4], vref[2] (+2)
-  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + 2 * GB + 8 + 4;
+  static constexpr int kRingOff = (kQOff + 2 * kQBytes + 1023) / 1024 * 1024;
+  // Behind the ring: factors, then floats xmax[2][GB][4], lpart[2][4][GB], mstat[2][GB],
+  // vmax[kGroups][2][4], qscale[2][kGroups], vstat[2][kGroups], then barriers and words.
+  static constexpr int kScBytes = E4M3 ? kScStages * 1024 : 0;
+  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + 2 * kGroups + 8 * kGroups + 2 * kGroups;
+  static constexpr int kFixedBars = 20 + 2 * kScStages;
+  static constexpr int kTailBytes = kScBytes + kMiscFloats * 4 + kFixedBars * 8 + 12 * 4;
+  static constexpr int kFit = (kSmemMax - kRingOff - kTailBytes) / (kTileBytes + 16);
+  static constexpr int kSlots = kFit > 24 ? 24 : kFit;
+  static constexpr int kScOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kMiscOff = kScOff + kScBytes;
   static constexpr int kBarOff = kMiscOff + kMiscFloats * 4;
-  static constexpr int kFixedBars = 22 + 2 * kScStages;
-  static constexpr int kTailBytes = kFixedBars * 8 + 16 * 4;  // then the ring's barriers
-  static constexpr int kRingBudget = 232448 - 1024 - (kBarOff + kTailBytes);
-  static constexpr int kSlotCost = kTileBytes + 16;
-  static constexpr int kSlots = kRingBudget / kSlotCost > 24 ? 24 : kRingBudget / kSlotCost;
-  static constexpr int kRingOff = (kBarOff + kTailBytes + kSlots * 16 + 1023) / 1024 * 1024;
-  static constexpr int kSmemBytes = kRingOff + kSlots * kTileBytes;
+  static constexpr int kSmemBytes = kScOff + kTailBytes + kSlots * 16;
   static constexpr int kTmemUse = 2 * (kQCols + kOCols);
   static constexpr int kTmemCols = kTmemUse <= 64 ? 64 : kTmemUse <= 128 ? 128 : kTmemUse <= 256 ? 256 : 512;
-  static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "swizzled buffers start on 1024 bytes");
-  static_assert(kSmemBytes <= 232448 && kSlots >= 4, "shared memory budget");
-  static_assert(kTmemUse <= 512, "tensor memory budget");
+  static_assert(kPBytes % 1024 == 0 && kQOff % 1024 == 0 && kBarOff % 16 == 0, "alignment");
+  static_assert(kSmemBytes <= kSmemMax && kSlots >= 3, "shared memory budget");
+  static_assert(kTmemCols * kCtas <= 512, "tensor memory budget");
+  // Warp roles behind the softmax warps; the epilogue's sit on the tensor memory lanes of
+  // their number mod 4.
+  static constexpr int kEpilogue = kSoftmaxWarps, kProducer = kEpilogue + 4, kIssuer = kProducer + 1,
+                       kQWarp = kProducer + 2, kScales = kProducer + 3;
 };
-
-constexpr int kDecodeThreads = 384;
-// Warps 0-3 softmax, 4-7 epilogue (each on the tensor memory lanes of its number mod 4).
-enum : int { kDecProducer = 8, kDecIssuer = 9, kDecQ = 10, kDecScales = 11 };
 
 enum DecodeTag : int {
   kTagDFull = 1, kTagDEmpty = 2, kTagDQ = 3, kTagDQEmpty = 4, kTagDS = 5, kTagDSEmpty = 6, kTagDP = 7, kTagDPEmpty = 8,
@@ -109,9 +126,27 @@ __device__ __forceinline__ void tma_load_4d(const CUtensorMap *m, uint64_t *bar,
       : "memory");
 }
 
-// make_sdesc with a 64-byte swizzle (mode 4): rows of 64 bytes, groups of 8 rows 512 bytes apart.
-__device__ __forceinline__ uint64_t make_sdesc64(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
-  return (make_sdesc(saddr, lbo_bytes, sbo_bytes) & ~(7ull << 61)) | (4ull << 61);
+// make_sdesc for rows of 32, 64 or 128 bytes, swizzled by their own width (modes 6, 4, 2).
+__device__ __forceinline__ uint64_t make_sdesc_row(int row_bytes, uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  const uint64_t mode = row_bytes == 128 ? 2 : row_bytes == 64 ? 4 : 6;
+  return (make_sdesc(saddr, lbo_bytes, sbo_bytes) & ~(7ull << 61)) | (mode << 61);
+}
+
+// Where byte `byte` of row `row` sits in such a tile: 16-byte chunks are exchanged by the
+// address bits above the row's 128-byte line.
+template <int ROW>
+__device__ __forceinline__ uint32_t swizzled(int row, int byte) {
+  const int f = ROW == 128 ? (row & 7) : ROW == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1);
+  return static_cast<uint32_t>(row * ROW + (byte ^ (f << 4)));
+}
+
+// mbar_wait with its slow path out of line (the waits are many, and instruction fetch is
+// what the roles of a CTA compete for).
+__device__ __noinline__ bool decode_wait_slow(const WaitCtx &c, uint64_t *bar, uint32_t parity, int tag) {
+  return mbar_wait(c, bar, parity, tag);
+}
+__device__ __forceinline__ bool decode_wait(const WaitCtx &c, uint64_t *bar, uint32_t parity, int tag) {
+  return mbar_try_wait(smem_u32(bar), parity) || decode_wait_slow(c, bar, parity, tag);
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
@@ -124,6 +159,37 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Two fp32 -> fp16x2, fp16x2 -> e4m3x2 (both to nearest even) and e4m3x2 -> fp16x2 (exact).
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+// 16 (a - b) on fp16 pairs.
+__device__ __forceinline__ uint32_t f16x2_rest(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
+      : "=r"(d)
+      : "r"(a), "r"(b), "r"(0x4c004c00u));
+  return d;
 }
 
 // Barrier `id` over `n` threads that also returns whether any of them passed true.
@@ -223,7 +289,7 @@ struct DecodeWalk {
 };
 
 template <int D, bool E4M3, int GB>
-__global__ void __launch_bounds__(kDecodeThreads, 1)
+__global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D, E4M3, GB>::kCtas)
     fa_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ DecodeParams p) {
   using C = DecodeCfg<D, E4M3, GB>;
@@ -245,14 +311,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(words);
   volatile int *abort_flag = words + 1;
   int *share = words + 2;  // b, x, off, tiles of this CTA's share, then T, nc and "do nothing"
-  uint64_t *bar_full = reinterpret_cast<uint64_t *>(words + 16);  // [kSlots]
+  uint64_t *bar_full = reinterpret_cast<uint64_t *>(words + 12);  // [kSlots]
   uint64_t *bar_empty = bar_full + C::kSlots;                     // [kSlots]
   float *xmax = reinterpret_cast<float *>(smem + C::kMiscOff);    // [2][GB][4]
   float *lpart = xmax + 2 * GB * 4;                               // [2][4][GB]
   float *mstat = lpart + 2 * 4 * GB;                              // [2][GB]
-  float *qscale = mstat + 2 * GB;                                 // [2][GB]
-  float *vmaxw = qscale + 2 * GB;                                 // [2][4]
-  float *vstat = vmaxw + 8;                                       // [2]
+  float *vmaxw = mstat + 2 * GB;                                  // [kGroups][2][4], read as float4 like xmax
+  float *qscale = vmaxw + 8 * C::kGroups;                         // [2][kGroups]
+  float *vstat = qscale + 2 * C::kGroups;                         // [2][kGroups]
+  static_assert(C::kMiscOff % 16 == 0 && (18 * GB) % 4 == 0, "xmax and vmaxw on 16 bytes");
   uint8_t *ring = smem + C::kRingOff;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
@@ -270,19 +337,20 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_q[i], 32);
-      mbar_init(&bar_q_empty[i], E4M3 ? 5 : 1);  // the issuer's commit; e4m3: and the softmax warps, for q's scale
+      // The issuer's commit; e4m3: and the softmax warps, for q's scale.
+      mbar_init(&bar_q_empty[i], 1 + (E4M3 ? C::kSoftmaxWarps : 0));
       mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_s_empty[i], 4);
-      mbar_init(&bar_p[i], 4);
+      mbar_init(&bar_s_empty[i], C::kSoftmaxWarps);
+      mbar_init(&bar_p[i], C::kSoftmaxWarps);
       mbar_init(&bar_p_empty[i], 1);
       mbar_init(&bar_o[i], 1);
       mbar_init(&bar_o_empty[i], 4);
-      mbar_init(&bar_stat[i], 4);
+      mbar_init(&bar_stat[i], C::kSoftmaxWarps);
     }
     mbar_init(bar_drain, 1);
     for (int i = 0; i < C::kScStages; ++i) {
       mbar_init(&bar_sc[i], 32);
-      mbar_init(&bar_sc_empty[i], 4);
+      mbar_init(&bar_sc_empty[i], C::kSoftmaxWarps);
     }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&bar_full[i], 1);
@@ -293,7 +361,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  if (warp == kDecIssuer) {
+  if (warp == C::kIssuer) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
@@ -303,7 +371,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // threads gives every share's first sequence.
   {
     const int items = p.c.H * p.nblk;
-    const int per = (p.c.B + kDecodeThreads - 1) / kDecodeThreads;
+    const int per = (p.c.B + C::kThreads - 1) / C::kThreads;
     const int b_lo = min(p.c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.c.B, b_lo + per);
     auto tiles_of = [&](int b) {
       const int len = cache_len(p.c, b, kKernelDecode);
@@ -318,11 +386,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
-    int *sums = reinterpret_cast<int *>(xmax);  // [12], used before the softmax warps start
+    int *sums = reinterpret_cast<int *>(xmax);  // [kWarps], used before the softmax warps start
+    static_assert(C::kWarps <= 2 * GB * 4, "the scan's sums fit");
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
     int before = 0, total = 0;
-    for (int w = 0; w < kDecodeThreads / 32; ++w) {
+    for (int w = 0; w < C::kWarps; ++w) {
       if (w < warp) before += sums[w];
       total += sums[w];
     }
@@ -356,7 +425,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   DecodeWalk wk;
   wk.start(p, share[0], share[1], share[2], share[6] ? 0 : share[3]);
 
-  if (warp == kDecProducer) {
+  if (warp == C::kProducer) {
     // ------------------------------------------------------------- producer
     // Lane i loads page i of a tile (pages of 128 rows or more: lane 0 alone).  The page
     // ids of the next tile are read while this tile's slots are waited for.
@@ -374,7 +443,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     };
     bool need, ok = true;
     int2 at = page_of(need);
-    int g = 0;  // slots filled so far
+    int g = 0, s = 0;        // slots filled so far, and the next one
+    uint32_t ph = 1;         // its "empty" phase: the first round passes at once
     while (wk.rem > 0 && ok) {
       const int h = wk.x / p.nblk;
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, need)) * rows * C::kRowBytes;
@@ -383,8 +453,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       wk.advance(p, 1);
       at = page_of(need);
       for (int kv = 0; kv < 2; ++kv, ++g) {
-        const int s = g % C::kSlots, r = g / C::kSlots;
-        if (r > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(ctx, &bar_empty[s], (r - 1) & 1, kTagDEmpty)))) break;
+        if (!(ok = __all_sync(0xffffffffu, decode_wait(ctx, &bar_empty[s], ph, kTagDEmpty)))) break;
         if (lane == 0) mbar_arrive_expect_tx(&bar_full[s], bytes);
         __syncwarp();
         if (now)
@@ -393,57 +462,68 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                         ring + s * C::kTileBytes + i * C::kPanelBytes + lane * rows * C::kPanelRow,
                         i * (C::kPanelRow / C::kElem), here.y, h, here.x);
         __syncwarp();
+        if (++s == C::kSlots) {
+          s = 0;
+          ph ^= 1;
+        }
       }
     }
     // The last loads have landed before the CTA can exit.
-    for (int s = 0; s < C::kSlots && s < g; ++s) mbar_drain(&bar_full[s], ((g - 1 - s) / C::kSlots) & 1);
+    for (int i = 0; i < C::kSlots && i < g; ++i) mbar_drain(&bar_full[i], ((g - 1 - i) / C::kSlots) & 1);
     __syncwarp();
-  } else if (warp == kDecIssuer) {
+  } else if (warp == C::kIssuer) {
     // --------------------------------------------------------------- issuer
     // S^T of tile i + 1 goes in ahead of V^T P of tile i, across segments too.
     constexpr uint32_t idesc_s = E4M3 ? make_idesc_e4m3(128, C::kQCols, 0, 0) : make_idesc_bf16(128, C::kQCols, 0, 0);
-    constexpr uint32_t idesc_o = E4M3 ? make_idesc_e4m3(128, C::kOCols, 1, 0) : make_idesc_bf16(128, C::kOCols, 1, 0);
-    constexpr bool kSw64 = C::kPanelRow == 64;
+    constexpr uint32_t idesc_o = E4M3 ? make_idesc_e4m3(128, C::kOCols, 1, 1) : make_idesc_bf16(128, C::kOCols, 1, 1);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t ring0 = smem_u32(ring);
-    // K (rows are keys) and Q (rows are heads) are K-major in the same panels.
-    const uint64_t k_desc0 = kSw64 ? make_sdesc64(ring0, 16, 512) : make_sdesc(ring0, 16, 1024);
-    const uint64_t q_desc0 = kSw64 ? make_sdesc64(smem_u32(smem + C::kQOff), 16, 512)
-                                   : make_sdesc(smem_u32(smem + C::kQOff), 16, 1024);
+    // K (rows are keys) and Q (rows are heads) are K-major in the same panels.  With 8 bf16
+    // rows of Q the 16 columns repeat them (row groups 0 bytes apart).
+    const uint64_t k_desc0 = make_sdesc_row(C::kPanelRow, ring0, 16, 8 * C::kPanelRow);
+    const uint64_t q_desc0 =
+        make_sdesc_row(C::kPanelRow, smem_u32(smem + C::kQOff), 16, C::kQRows < 16 ? 0 : 8 * C::kPanelRow);
     // V as the M x K operand V^T is MN-major.  M = 128 features are d = 128's, in panels
     // kPanelBytes apart; for d = 64 the second half repeats the first (offset 0), and its
     // half of O^T is not read.
-    constexpr uint32_t v_lbo = D == 128 ? C::kPanelBytes : 0;
-    const uint64_t v_desc0 = kSw64 ? make_sdesc64(ring0, v_lbo, 512) : make_sdesc(ring0, v_lbo, 1024);
-    const uint64_t p_desc0 = make_sdesc(smem_u32(smem + C::kPOff), 16, 1024);
+    const uint64_t v_desc0 = make_sdesc_row(C::kPanelRow, ring0, D == 128 ? C::kPanelBytes : 0, 8 * C::kPanelRow);
+    // P as the K x N operand is MN-major too, one row of kPRow bytes per key.
+    const uint64_t p_desc0 = make_sdesc_row(C::kPRow, smem_u32(smem + C::kPOff), 16, 8 * C::kPRow);
     bool ok = true;
-    auto wait = [&](uint64_t *bar, int parity, int tag) {
-      return __all_sync(0xffffffffu, mbar_wait(ctx, bar, static_cast<uint32_t>(parity), tag));
+    auto wait = [&](uint64_t *bar, uint32_t parity, int tag) {
+      return __all_sync(0xffffffffu, decode_wait(ctx, bar, parity, tag));
+    };
+    int s = 0;          // ring slot of the next K; its V is in the next one
+    uint32_t ph = 0;    // the slot's "full" phase
+    auto next_slot = [&]() {
+      if (++s == C::kSlots) {
+        s = 0;
+        ph ^= 1;
+      }
     };
     int n = 0;  // tiles whose S^T was issued
     // What V^T P of the previous tile needs to know.
     bool pend = false, pend_first = false, pend_last = false;
-    int pend_seg = 0;
+    int pend_seg = 0, pend_s = 0;
+    uint32_t pend_ph = 0;
     auto issue_o = [&](int i) {  // tile i's V^T P
-      const int buf = i & 1, g = 2 * i + 1, s = g % C::kSlots, ob = pend_seg & 1;
+      const int buf = i & 1, ob = pend_seg & 1;
       if (pend_first && pend_seg >= 2 && !wait(&bar_o_empty[ob], ((pend_seg >> 1) - 1) & 1, kTagDOEmpty)) return false;
-      if (!wait(&bar_full[s], (g / C::kSlots) & 1, kTagDFull)) return false;
+      if (!wait(&bar_full[pend_s], pend_ph, kTagDFull)) return false;
       if (!wait(&bar_p[buf], (i >> 1) & 1, kTagDP)) return false;
       tc_fence_after();
-      const uint64_t vd = sdesc_add(v_desc0, s * C::kTileBytes), pd = sdesc_add(p_desc0, buf * C::kPBytes);
+      const uint64_t vd = sdesc_add(v_desc0, pend_s * C::kTileBytes), pd = sdesc_add(p_desc0, buf * C::kPBytes);
       const uint32_t to = tm + kOCol0 + ob * C::kOCols;
-      if constexpr (E4M3) {
+      constexpr int kStep = E4M3 ? 32 : 16;  // keys per instruction
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)  // 32 keys each
-          mma_ss_f8_w(to, sdesc_add(vd, ks * 32 * C::kPanelRow), sdesc_add(pd, ks * 32), idesc_o,
-                      (!pend_first || ks > 0) ? 1u : 0u);
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)  // 16 keys each; P's panels hold 64
-          mma_ss_w(to, sdesc_add(vd, ks * 16 * 128), sdesc_add(pd, (ks >> 2) * C::kOCols * 128 + (ks & 3) * 32),
-                   idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
+      for (int ks = 0; ks < 128 / kStep; ++ks) {
+        const uint64_t a = sdesc_add(vd, ks * kStep * C::kPanelRow), b = sdesc_add(pd, ks * kStep * C::kPRow);
+        if constexpr (E4M3)
+          mma_ss_f8_w(to, a, b, idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
+        else
+          mma_ss_w(to, a, b, idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
       }
-      mma_commit_w(&bar_empty[s]);
+      mma_commit_w(&bar_empty[pend_s]);
       mma_commit_w(&bar_p_empty[buf]);
       if (pend_last) mma_commit_w(&bar_o[ob]);
       return true;
@@ -452,33 +532,33 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const int run = wk.run(), qb = seg & 1;
       if (!(ok = wait(&bar_q[qb], (seg >> 1) & 1, kTagDQ))) break;
       for (int i = 0; i < run && ok; ++i, ++n) {
-        const int buf = n & 1, g = 2 * n, s = g % C::kSlots;
+        const int buf = n & 1;
         if (n >= 2 && !(ok = wait(&bar_s_empty[buf], ((n >> 1) - 1) & 1, kTagDSEmpty))) break;
-        if (!(ok = wait(&bar_full[s], (g / C::kSlots) & 1, kTagDFull))) break;
+        if (!(ok = wait(&bar_full[s], ph, kTagDFull))) break;
         tc_fence_after();
         const uint64_t kd = sdesc_add(k_desc0, s * C::kTileBytes), qd = sdesc_add(q_desc0, qb * C::kQBytes);
         const uint32_t ts = tm + buf * C::kQCols;
-        if constexpr (E4M3) {
 #pragma unroll
-          for (int ks = 0; ks < D / 32; ++ks)
-            mma_ss_f8_w(ts, sdesc_add(kd, ks * 32), sdesc_add(qd, ks * 32), idesc_s, ks > 0);
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss_w(ts, sdesc_add(kd, (ks >> 2) * C::kPanelBytes + (ks & 3) * 32),
-                     sdesc_add(qd, (ks >> 2) * C::kQCols * 128 + (ks & 3) * 32), idesc_s, ks > 0);
+        for (int ks = 0; ks < C::kRowBytes / 32; ++ks) {  // 32 bytes of the rows per instruction
+          const uint64_t a = sdesc_add(kd, (ks >> 2) * C::kPanelBytes + (ks & 3) * 32);
+          const uint64_t b = sdesc_add(qd, (ks >> 2) * C::kQRows * C::kPanelRow + (ks & 3) * 32);
+          if constexpr (E4M3)
+            mma_ss_f8_w(ts, a, b, idesc_s, ks > 0);
+          else
+            mma_ss_w(ts, a, b, idesc_s, ks > 0);
         }
         mma_commit_w(&bar_empty[s]);
         mma_commit_w(&bar_s[buf]);
         if (i + 1 == run) mma_commit_w(&bar_q_empty[qb]);
-        if (pend && !(ok = issue_o(n - 1))) {
-          ++n;
-          break;
-        }
+        if (pend && !(ok = issue_o(n - 1))) break;
         pend = true;
         pend_first = i == 0;
         pend_last = i + 1 == run;
         pend_seg = seg;
+        next_slot();
+        pend_s = s;
+        pend_ph = ph;
+        next_slot();
       }
       if (ok) wk.advance(p, run);
     }
@@ -488,91 +568,97 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       mbar_drain(bar_drain, 0);
     }
     __syncwarp();
-  } else if (warp == kDecQ) {
+  } else if (warp == C::kQWarp) {
     // ---------------------------------------------------------------- Q rows
-    // Rows of the segment's query heads into swizzled shared memory; the next segment's
-    // rows are read while this one's buffer is waited for.  Rows past the last head are 0.
+    // Rows of the segment's query heads into swizzled shared memory, 8 at a time; the next
+    // 8 (of this segment or the next) are read meanwhile.  Rows past the last head are 0.
     constexpr int kWords = D / 64;  // 32-bit words (2 elements) of a row per lane
-    uint32_t w[GB][kWords];
-    auto load = [&]() {
-      const int h = wk.x / p.nblk, g0 = (wk.x % p.nblk) * GB;
+    uint32_t w[8][kWords];
+    auto load = [&](int c) {
+      const int h = wk.x / p.nblk, g0 = (wk.x % p.nblk) * GB + 8 * c;
       const uint32_t *src = reinterpret_cast<const uint32_t *>(
-          p.q + (static_cast<long long>(wk.b) * p.Hq + h * p.G + g0) * D);
+          p.q + (static_cast<long long>(wk.b) * p.Hq + h * p.G + g0) * D) + lane * kWords;
 #pragma unroll
-      for (int r = 0; r < GB; ++r)
+      for (int r = 0; r < 8; ++r) {
+        const bool live = wk.rem > 0 && g0 + r < p.G;
 #pragma unroll
-        for (int i = 0; i < kWords; ++i)
-          w[r][i] = (wk.rem > 0 && g0 + r < p.G) ? __ldg(src + r * (D / 2) + lane * kWords + i) : 0u;
+        for (int i = 0; i < kWords; ++i) w[r][i] = live ? __ldg(src + r * (D / 2) + i) : 0u;
+      }
     };
     bool ok = true;
-    load();
+    load(0);
     for (int seg = 0; wk.rem > 0 && ok; ++seg) {
       const int qb = seg & 1;
-      if (seg >= 2 && !(ok = __all_sync(0xffffffffu, mbar_wait(ctx, &bar_q_empty[qb], ((seg >> 1) - 1) & 1, kTagDQEmpty))))
+      if (seg >= 2 && !(ok = __all_sync(0xffffffffu, decode_wait(ctx, &bar_q_empty[qb], ((seg >> 1) - 1) & 1, kTagDQEmpty))))
         break;
       uint8_t *dst = smem + C::kQOff + qb * C::kQBytes;
-      if constexpr (!E4M3) {
+#pragma unroll 1
+      for (int c = 0; c < C::kGroups; ++c) {
+        uint32_t v[8][kWords];
 #pragma unroll
-        for (int r = 0; r < C::kQCols; ++r) {
-          // Lane's elements start at byte lane * 4 * kWords of the row.
-          const int byte = lane * 4 * kWords, panel = byte >> 7, in = byte & 127;
-          uint8_t *at = dst + panel * (C::kQCols * 128) + r * 128 + ((((in >> 4) ^ (r & 7)) << 4) | (in & 15));
+        for (int r = 0; r < 8; ++r)
 #pragma unroll
-          for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(at)[i] = r < GB ? w[r < GB ? r : 0][i] : 0u;
+          for (int i = 0; i < kWords; ++i) v[r][i] = w[r][i];
+        if (c + 1 < C::kGroups) {
+          load(c + 1);
+        } else {
+          wk.advance(p, wk.run());
+          load(0);
         }
-      } else {
-        // Scale each row by the power of two that brings its largest element into
-        // [128, 256), then split: hi = e4m3(x), lo = e4m3(16 (x - hi)).
-        float x[2 * kWords];
+        if constexpr (!E4M3) {
+          const int byte = lane * 4 * kWords;  // this lane's elements in the row
 #pragma unroll
-        for (int r = 0; r < GB; ++r) {
+          for (int r = 0; r < 8; ++r) {
+            uint8_t *at = dst + (byte >> 7) * (C::kQRows * 128) + swizzled<128>(8 * c + r, byte & 127);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(at)[i] = v[r][i];
+          }
+        } else {
+          // Scale the 8 rows by the power of two that brings their largest element into
+          // [128, 256), then split: hi = e4m3(x), lo = e4m3(16 (x - hi)).  A row's scores
+          // are off by at most 2^-20 of the group's largest.
           float m = 0.f;
 #pragma unroll
-          for (int i = 0; i < kWords; ++i) {
-            x[2 * i] = bf16_lo(w[r][i]);
-            x[2 * i + 1] = bf16_hi(w[r][i]);
-            m = fmaxf(m, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-          }
+          for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(v[r][i])), fabsf(bf16_hi(v[r][i]))));
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // Exponent field e of m: m in [2^(e-127), 2^(e-126)); x * 2^(134 - e).
-          // An infinity (e = 255) makes every score of the head NaN.
+          // m in [2^(e-127), 2^(e-126)); x * 2^(134 - e).  An infinity (e = 255) makes every
+          // score NaN, as a NaN does by itself.
           const int e0 = static_cast<int>(__float_as_uint(m) >> 23), e = min(max(e0, 16), 250);
           const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
           if (lane == 0)
-            qscale[qb * GB + r] =
+            qscale[qb * C::kGroups + c] =
                 __uint_as_float(e0 == 255 ? 0x7fc00000u : static_cast<uint32_t>(e - 7) << 23) * p.scale_log2;
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) {
-            const float a = x[2 * i] * up, c = x[2 * i + 1] * up;
-            const uint32_t h2 = pack_e4m3x4(a, c, 0.f, 0.f);
-            const float2 back = e4m3x2_to_float2(static_cast<uint16_t>(h2));
-            const uint32_t l2 = pack_e4m3x4((a - back.x) * 16.f, (c - back.y) * 16.f, 0.f, 0.f);
-            hi |= h2 << (16 * i);
-            lo |= l2 << (16 * i);
-          }
           const int byte = lane * 2 * kWords;
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const int row = part * GB + r;
-            const uint32_t v = part == 0 ? hi : lo;
-            const int chunk = C::kPanelRow == 64 ? ((byte >> 4) ^ ((row >> 1) & 3)) : ((byte >> 4) ^ (row & 7));
-            uint8_t *at = dst + row * C::kPanelRow + ((chunk << 4) | (byte & 15));
-            if constexpr (kWords == 2)
-              *reinterpret_cast<uint32_t *>(at) = v;
-            else
-              *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(v);
+          for (int r = 0; r < 8; ++r) {
+            uint32_t part[2] = {0u, 0u};
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+              const float a = bf16_lo(v[r][i]) * up, b = bf16_hi(v[r][i]) * up;
+              const uint32_t h2 = pack_e4m3x4(a, b, 0.f, 0.f);
+              const float2 back = e4m3x2_to_float2(static_cast<uint16_t>(h2));
+              part[0] |= h2 << (16 * i);
+              part[1] |= pack_e4m3x4((a - back.x) * 16.f, (b - back.y) * 16.f, 0.f, 0.f) << (16 * i);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint8_t *at = dst + swizzled<C::kPanelRow>(k * GB + 8 * c + r, byte);
+              if constexpr (kWords == 2)
+                *reinterpret_cast<uint32_t *>(at) = part[k];
+              else
+                *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(part[k]);
+            }
           }
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(&bar_q[qb]);
-      wk.advance(p, wk.run());
-      load();
     }
     __syncwarp();
-  } else if (warp == kDecScales) {
+  } else if (warp == C::kScales) {
     // ------------------------------------------------- the keys' factors (e4m3)
     if constexpr (E4M3) {
       // Lane i copies the factors of keys i, i + 32, ... of a tile; the next tile's page
@@ -586,12 +672,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if (wk.rem > 0 && pos >= wk.first && pos < wk.len) page[i] = cache_page(p.c, wk.b, pos, row[i], kKernelDecode);
         }
       };
-      bool ok = true;
       pages_of();
       for (int n = 0; wk.rem > 0; ++n) {
         const int st = n % C::kScStages;
         if (n >= C::kScStages &&
-            !(ok = __all_sync(0xffffffffu, mbar_wait(ctx, &bar_sc_empty[st], (n / C::kScStages - 1) & 1, kTagDScEmpty))))
+            !__all_sync(0xffffffffu, decode_wait(ctx, &bar_sc_empty[st], (n / C::kScStages - 1) & 1, kTagDScEmpty)))
           break;
         const int h = wk.x / p.nblk;
         const uint32_t dst = smem_u32(smem + C::kScOff) + st * 1024;
@@ -612,106 +697,123 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
     }
-  } else if (warp < 4) {
+  } else if (warp < C::kSoftmaxWarps) {
     // -------------------------------------------------------------- softmax
-    // Thread = key (row of S^T, tensor memory lane 32 * warp + lane), GB scores each.
-    // All waits are bounded and every thread reaches every bar_any, so a failed wait
-    // (`bad`) ends the four warps together.
-    const int key = warp * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    float mref[GB], l[GB];
-    float vref = 1.f;  // e4m3: power of two that V's factors are taken relative to
+    // Thread = key (row of S^T, tensor memory lane) and group of 8 heads, kept in pairs.
+    // All waits are bounded and every thread of the group reaches every bar_any, so a
+    // failed wait (`bad`) ends the group's four warps together.
+    const int grp = warp >> 2, w4 = warp & 3, key = w4 * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t bar_a = 1 + 2 * grp, bar_b = 2 + 2 * grp;
+    float *xm = xmax + 8 * grp * 4;
+    uint64_t nm2[4], l2[4];           // minus the reference, and this key's sum of weights
+    float vref = 1.f, vinv = 1.f;     // e4m3: power of two that V's factors are taken relative to; kWeight / vref
     bool bad = false, stop = false;
-    int n = 0, nred = 0;
+    int n = 0, nred = 0, sv = 1;      // tiles, reductions, ring slot of the tile's V
+    uint32_t vph = 0;
     for (int seg = 0; wk.rem > 0 && !stop; ++seg) {
       const int run = wk.run(), qb = seg & 1;
-      float qs[E4M3 ? GB : 1];
+      float qs = p.scale_log2;
       if constexpr (E4M3) {
-        bad |= !mbar_wait(ctx, &bar_q[qb], (seg >> 1) & 1, kTagDQ);
-#pragma unroll
-        for (int g = 0; g < GB; ++g) qs[g] = qscale[qb * GB + g];
+        bad |= !decode_wait(ctx, &bar_q[qb], (seg >> 1) & 1, kTagDQ);
+        qs = qscale[qb * C::kGroups + grp];
       }
 #pragma unroll
-      for (int g = 0; g < GB; ++g) {
-        mref[g] = -INFINITY;
-        l[g] = 0.f;
-      }
+      for (int i = 0; i < 4; ++i) nm2[i] = l2[i] = 0ull;
+#pragma unroll 1
       for (int i = 0; i < run; ++i, ++n) {
         const int buf = n & 1;
-        const int pos0 = (wk.tile0 + wk.off + i) * 128, pos = pos0 + key;
-        const bool partial = pos0 < wk.first || pos0 + 128 > wk.len;
-        const bool valid = pos >= wk.first && pos < wk.len;
-        bad |= !mbar_wait(ctx, &bar_s[buf], (n >> 1) & 1, kTagDS);
-        if (n >= 2) bad |= !mbar_wait(ctx, &bar_p_empty[buf], ((n >> 1) - 1) & 1, kTagDPEmpty);
-        float fk = p.scale_log2, fv = 1.f;
+        const int pos0 = (wk.tile0 + wk.off + i) * 128;
+        bad |= !decode_wait(ctx, &bar_s[buf], (n >> 1) & 1, kTagDS);
+        if (n >= 2) bad |= !decode_wait(ctx, &bar_p_empty[buf], ((n >> 1) - 1) & 1, kTagDPEmpty);
+        float f = qs, fv = 1.f;
         if constexpr (E4M3) {
           const int st = n % C::kScStages;
-          bad |= !mbar_wait(ctx, &bar_sc[st], (n / C::kScStages) & 1, kTagDSc);
+          bad |= !decode_wait(ctx, &bar_sc[st], (n / C::kScStages) & 1, kTagDSc);
           const float *sc = reinterpret_cast<const float *>(smem + C::kScOff + st * 1024);
-          fk = sc[key];
+          f = qs * sc[key];
           fv = sc[128 + key];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_sc_empty[st]);
-        }
-        if (partial) {
-          // Masked rows of V: weight 0 times whatever the page holds has to be 0.
-          const int gv = 2 * n + 1, sv = gv % C::kSlots;
-          bad |= !mbar_wait(ctx, &bar_full[sv], (gv / C::kSlots) & 1, kTagDFull);
-          if (!valid) {
-            uint8_t *rowp = ring + sv * C::kTileBytes + key * C::kPanelRow;
-#pragma unroll
-            for (int ch = 0; ch < C::kRowBytes / 16; ++ch) {
-              // Lanes start at different chunks, so that their stores fall into different banks.
-              const int c = (ch + lane) % (C::kRowBytes / 16);
-              *reinterpret_cast<uint4 *>(rowp + (c * 16 / C::kPanelRow) * C::kPanelBytes + (c * 16) % C::kPanelRow) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
         }
         __syncwarp();
         tc_fence_after();
-        float s[GB];
+        uint64_t v2[4];  // scores before their factor
         {
-          const uint32_t ts = tmem + lane_off + buf * C::kQCols;
-          uint32_t raw[C::kQCols < GB ? GB : (E4M3 ? 2 * GB : GB)];
-#pragma unroll
-          for (int c = 0; c < (E4M3 ? 2 * GB : GB); c += 8) tmem_ld8(ts + c, raw + c);
+          const uint32_t ts = tmem + lane_off + buf * C::kQCols + 8 * grp;
+          uint32_t hi[8], lo[8];
+          tmem_ld8(ts, hi);
+          if constexpr (E4M3) tmem_ld8(ts + GB, lo);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_s_empty[buf]);
+          if (lane == 0) {
+            mbar_arrive(&bar_s_empty[buf]);
+            if constexpr (E4M3) mbar_arrive(&bar_sc_empty[n % C::kScStages]);
+          }
 #pragma unroll
-          for (int g = 0; g < GB; ++g) {
-            float v = __uint_as_float(raw[g]);
-            if constexpr (E4M3) v = fmaf(__uint_as_float(raw[GB + g]), 0.0625f, v) * qs[g];
-            s[g] = valid ? v * fk : -INFINITY;
+          for (int g = 0; g < 4; ++g) {
+            v2[g] = f2pack(__uint_as_float(hi[2 * g]), __uint_as_float(hi[2 * g + 1]));
+            if constexpr (E4M3)
+              v2[g] = ffma2(f2pack(__uint_as_float(lo[2 * g]), __uint_as_float(lo[2 * g + 1])), f2pack(0.0625f, 0.0625f),
+                            v2[g]);
           }
         }
-        // Does a score outgrow the reference?
-        bool grow = i == 0;
+        if (pos0 < wk.first || pos0 + 128 > wk.len) {
+          const int pos = pos0 + key;
+          const bool valid = pos >= wk.first && pos < wk.len;
+          if (!valid) {
+            f = 1.f;
+            fv = 0.f;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v2[g] = f2pack(-INFINITY, -INFINITY);
+          }
+          // Masked rows of V: weight 0 times whatever the page holds has to be 0.
+          if (grp == 0) {
+            bad |= !decode_wait(ctx, &bar_full[sv], vph, kTagDFull);
+            if (!valid) {
+              uint8_t *rowp = ring + sv * C::kTileBytes + key * C::kPanelRow;
+#pragma unroll 1
+              for (int ch = 0; ch < C::kRowBytes / 16; ++ch) {
+                // Lanes start at different chunks, so that their stores fall into different banks.
+                const int c = (ch + lane) % (C::kRowBytes / 16);
+                *reinterpret_cast<uint4 *>(rowp + (c * 16 / C::kPanelRow) * C::kPanelBytes + (c * 16) % C::kPanelRow) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        const uint64_t f2 = f2pack(f, f);
+        float x[8];  // log2 of the weights
+        bool grow = true;
         if (i > 0) {
 #pragma unroll
-          for (int g = 0; g < GB; ++g) grow |= s[g] > mref[g] + C::kGrow;
-          if constexpr (E4M3) grow |= valid && fabsf(fv) > vref;
+          for (int g = 0; g < 4; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
+          const float top = fmaxf(fmax3(fmax3(x[0], x[1], x[2]), x[3], x[4]), fmax3(x[5], x[6], x[7]));
+          grow = top > C::kGrow;
+          if constexpr (E4M3) grow |= fabsf(fv) > vref;
+          grow = bar_any(bar_a, 128, grow || bad);
         }
-        if (i == 0 || bar_any(1, 128, grow || bad)) {
-          float *xm = xmax + (nred & 1) * GB * 4;
-          float v[GB];
+        if (grow) {
+          // The reference moves (or a segment begins) to the maximum over the keys so far.
+          float *xr = xm + (nred & 1) * GB * 4;
+          float *vr = vmaxw + grp * 8 + (nred & 1) * 4;
+          ++nred;
+          float v[8];
 #pragma unroll
-          for (int g = 0; g < GB; ++g) v[g] = s[g];
-          reduce_columns<GB>(v, [](float a, float b) { return fmaxf(a, b); });
-          if ((lane & (32 / GB - 1)) == 0) xm[(lane / (32 / GB)) * 4 + warp] = v[0];
+          for (int g = 0; g < 4; ++g) f2unpack(fmul2(v2[g], f2), v[2 * g], v[2 * g + 1]);
+          reduce_columns<8>(v, [](float a, float b) { return fmaxf(a, b); });
+          if ((lane & 3) == 0) xr[lane + w4] = v[0];
           if constexpr (E4M3) {
-            const uint32_t vm = __reduce_max_sync(0xffffffffu, valid ? __float_as_uint(fabsf(fv)) : 0u);
-            if (lane == 0) vmaxw[(nred & 1) * 4 + warp] = __uint_as_float(vm);
+            const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
+            if (lane == 0) vr[w4] = __uint_as_float(vm);
           }
-          if (bar_any(2, 128, bad)) {
+          if (bar_any(bar_b, 128, bad)) {
             stop = true;
             break;
           }
-          float alpha[GB], vscale = 1.f;
+          float vscale = 1.f;
           if constexpr (E4M3) {
-            const float4 v4 = *reinterpret_cast<const float4 *>(vmaxw + (nred & 1) * 4);
+            const float4 v4 = *reinterpret_cast<const float4 *>(vr);
             const uint32_t top = __float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)));
             // The next power of two, within [2^-120, 2^126].
             const uint32_t up = (min(top, 0x7e800000u) + 0x7fffffu) & 0x7f800000u;
@@ -721,103 +823,107 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
               vscale = vref / now;
             }
             vref = now;
+            vinv = C::kWeight / now;
           }
+          // Column lane / 4's maximum; -1e30 stands in for -inf, so that differences stay defined.
+          const float4 m4 = *reinterpret_cast<const float4 *>(xr + (lane & ~3));
+          const float mc = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -1e30f);
+          float alpha[8];
 #pragma unroll
-          for (int g = 0; g < GB; ++g) {
-            const float4 m4 = *reinterpret_cast<const float4 *>(xm + g * 4);
-            const float m = fmaxf(fmaxf(mref[g], m4.x), fmaxf(fmaxf(m4.y, m4.z), m4.w));
-            alpha[g] = (i == 0 || m == mref[g]) ? 1.f : ex2(mref[g] - m);
-            mref[g] = m;
-            l[g] *= alpha[g];
+          for (int g = 0; g < 4; ++g) {
+            float a, b;
+            f2unpack(nm2[g], a, b);
+            float m0 = __shfl_sync(0xffffffffu, mc, 8 * g), m1 = __shfl_sync(0xffffffffu, mc, 8 * g + 4);
+            if (i > 0) {
+              m0 = fmaxf(m0, -a);
+              m1 = fmaxf(m1, -b);
+            }
+            alpha[2 * g] = ex2(-a - m0);
+            alpha[2 * g + 1] = ex2(-b - m1);
+            nm2[g] = f2pack(-m0, -m1);
+            if (i > 0) l2[g] = fmul2(l2[g], f2pack(alpha[2 * g], alpha[2 * g + 1]));
           }
-          ++nred;
           if (i > 0) {
             // O holds tiles of this segment on the old reference: bring it to the new one.
-            bad |= !mbar_wait(ctx, &bar_p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kTagDPEmpty);
+            bad |= !decode_wait(ctx, &bar_p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kTagDPEmpty);
+            __syncwarp();
             tc_fence_after();
-            const uint32_t to = tmem + lane_off + kOCol0 + (seg & 1) * C::kOCols;
+            const uint32_t to = tmem + lane_off + kOCol0 + (seg & 1) * C::kOCols + 8 * grp;
+#pragma unroll 1
+            for (int part = 0; part < C::kOParts; ++part) {
+              uint32_t o[8];
+              tmem_ld8(to + part * GB, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int part = 0; part < C::kOParts; ++part)
-#pragma unroll
-              for (int g = 0; g < GB; g += 8) {
-                uint32_t o[8];
-                tmem_ld8(to + part * GB + g, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha[g + e] * vscale));
-                tmem_st8(to + part * GB + g, o);
-              }
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha[e] * vscale));
+              tmem_st8(to + part * GB, o);
+            }
             tmem_wait_st();
             tc_fence_before();
           }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
         }
-        // Weights into P: row (part, head), column key.
+        // Weights into P: row = key, this group's 8 heads of each part.
         const uint32_t pb = smem_u32(smem + C::kPOff) + buf * C::kPBytes;
-        float pw[GB];
+        uint32_t part[C::kOParts][4];
 #pragma unroll
-        for (int g = 0; g < GB; ++g) {
-          pw[g] = ex2(s[g] - (mref[g] == -INFINITY ? 0.f : mref[g]));
-          l[g] += pw[g];
-        }
-        if constexpr (!E4M3) {
-          const uint32_t a0 = pb + (key >> 6) * (C::kOCols * 128) + ((key & 63) >> 3) * 16 + (key & 7) * 2;
+        for (int g = 0; g < 4; ++g) {
+          const float a = ex2(x[2 * g]), b = ex2(x[2 * g + 1]);
+          l2[g] = fadd2(l2[g], f2pack(a, b));
+          if constexpr (!E4M3) {
+            part[0][g] = pack_bf16(a, b);
+            part[1][g] = pack_bf16(a - bf16_lo(part[0][g]), b - bf16_hi(part[0][g]));
+          } else {
+            const float fw = fv * vinv;
+            uint32_t r = pack_f16(a * fw, b * fw);
 #pragma unroll
-          for (int g = 0; g < GB; g += 2) {
-            const uint32_t hi = pack_bf16(pw[g], pw[g + 1]);
-            const uint32_t lo = pack_bf16(pw[g] - bf16_lo(hi), pw[g + 1] - bf16_hi(hi));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r0 = g + e, r1 = GB + g + e;
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"((a0 ^ ((r0 & 7) << 4)) + r0 * 128),
-                           "h"(static_cast<uint16_t>(e ? hi >> 16 : hi))
-                           : "memory");
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"((a0 ^ ((r1 & 7) << 4)) + r1 * 128),
-                           "h"(static_cast<uint16_t>(e ? lo >> 16 : lo))
-                           : "memory");
+            for (int k = 0; k < 3; ++k) {
+              const uint16_t c = f16x2_to_e4m3x2(r);
+              part[k][g] = c;
+              if (k < 2) r = f16x2_rest(r, e4m3x2_to_f16x2(c));
             }
           }
+        }
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            st_shared_v4(pb + swizzled<C::kPRow>(key, 2 * (k * GB + 8 * grp)), part[k][0], part[k][1], part[k][2], part[k][3]);
         } else {
-          const float fw = valid ? fv * (C::kWeight / vref) : 0.f;
-          const uint32_t a0 = pb + (key >> 4) * 16 + (key & 15);
 #pragma unroll
-          for (int g = 0; g < GB; g += 4) {
-            float r[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = pw[g + e] * fw;
-#pragma unroll
-            for (int part = 0; part < 3; ++part) {
-              const uint32_t code = pack_e4m3x4(r[0], r[1], r[2], r[3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int row = part * GB + g + e;
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"((a0 ^ ((row & 7) << 4)) + row * 128), "r"(code >> (8 * e))
-                             : "memory");
-              }
-              if (part < 2) {
-                const float2 lo2 = e4m3x2_to_float2(static_cast<uint16_t>(code));
-                const float2 hi2 = e4m3x2_to_float2(static_cast<uint16_t>(code >> 16));
-                r[0] = (r[0] - lo2.x) * 16.f;
-                r[1] = (r[1] - lo2.y) * 16.f;
-                r[2] = (r[2] - hi2.x) * 16.f;
-                r[3] = (r[3] - hi2.y) * 16.f;
-              }
-            }
+          for (int k = 0; k < 3; ++k) {
+            const int byte = k * GB + 8 * grp;
+            const uint32_t at = pb + swizzled<C::kPRow>(key, byte & ~15) + (byte & 8);
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(part[k][0] | (part[k][1] << 16)),
+                         "r"(part[k][2] | (part[k][3] << 16))
+                         : "memory");
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_p[buf]);
+        if ((sv += 2) >= C::kSlots) {
+          sv -= C::kSlots;
+          vph ^= 1;
+        }
       }
       if (stop) break;
       // The segment's statistics for the epilogue.
       const int ob = seg & 1;
-      if (seg >= 2) bad |= !mbar_wait(ctx, &bar_o_empty[ob], ((seg >> 1) - 1) & 1, kTagDOEmpty);
-      reduce_columns<GB>(l, [](float a, float b) { return a + b; });
-      if ((lane & (32 / GB - 1)) == 0) lpart[(ob * 4 + warp) * GB + lane / (32 / GB)] = l[0];
-      if (threadIdx.x == 0) {
+      if (seg >= 2) bad |= !decode_wait(ctx, &bar_o_empty[ob], ((seg >> 1) - 1) & 1, kTagDOEmpty);
+      __syncwarp();
+      float l[8], m[8];
 #pragma unroll
-        for (int g = 0; g < GB; ++g) mstat[ob * GB + g] = mref[g];
-        if constexpr (E4M3) vstat[ob] = vref;
+      for (int g = 0; g < 4; ++g) {
+        f2unpack(l2[g], l[2 * g], l[2 * g + 1]);
+        f2unpack(nm2[g], m[2 * g], m[2 * g + 1]);
+      }
+      reduce_columns<8>(l, [](float a, float b) { return a + b; });
+      if ((lane & 3) == 0) lpart[(ob * 4 + w4) * GB + 8 * grp + (lane >> 2)] = l[0];
+      if (w4 == 0 && lane == 0) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) mstat[ob * GB + 8 * grp + g] = -m[g];
+        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = 1.f / vinv;
       }
       __syncwarp();
       if (lane == 0) {
@@ -830,8 +936,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   } else {
     // ------------------------------------------------------------- epilogue
     // Thread = feature (tensor memory lane).  Idle sequences first: o = 0, lse = -inf.
-    const int f = (warp - 4) * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>((warp - 4) * 32) << 16;
+    const int f = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
       if (cache_len(p.c, b, kKernelDecode) > 0) continue;
       const long long row0 = static_cast<long long>(b) * p.Hq;
@@ -847,37 +953,45 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       const int ob = seg & 1, run = wk.run();
       const int h = wk.x / p.nblk, g0 = (wk.x % p.nblk) * GB, ng = min(GB, p.G - g0);
       const bool starts = wk.off == 0, ends = wk.off + run == wk.n;
-      ok = __all_sync(0xffffffffu, mbar_wait(ctx, &bar_stat[ob], (seg >> 1) & 1, kTagDStat) &&
-                                       mbar_wait(ctx, &bar_o[ob], (seg >> 1) & 1, kTagDO));
+      ok = __all_sync(0xffffffffu, decode_wait(ctx, &bar_stat[ob], (seg >> 1) & 1, kTagDStat) &&
+                                       decode_wait(ctx, &bar_o[ob], (seg >> 1) & 1, kTagDO));
       if (!ok) break;
       tc_fence_after();
       const uint32_t to = tmem + lane_off + kOCol0 + ob * C::kOCols;
-      const float unit = E4M3 ? vstat[ob] * (1.f / C::kWeight) : 1.f;
       const long long row0 = static_cast<long long>(wk.b) * p.Hq + h * p.G + g0;
       const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
-#pragma unroll
+      const bool whole = starts && ends;
+#pragma unroll 1
       for (int gc = 0; gc < GB; gc += 8) {
         uint32_t o[C::kOParts][8];
 #pragma unroll
         for (int part = 0; part < C::kOParts; ++part) tmem_ld8(to + part * GB + gc, o[part]);
+        // Lane g < 8 has head gc + g's sums.
+        const float *lp = lpart + ob * 4 * GB + gc + (lane & 7);
+        const float lt = (lp[0] + lp[GB]) + (lp[2 * GB] + lp[3 * GB]);
+        const float mt8 = mstat[ob * GB + gc + (lane & 7)];
+        float mul = E4M3 ? vstat[ob * C::kGroups + gc / 8] : 1.f;
+        if (whole) mul /= lt;
+        if ((warp & 3) == 0 && lane < 8 && gc + lane < ng) {
+          if (!whole)
+            p.part_ml[slot * GB + gc + lane] = make_float2(mt8, lt);
+          else if (p.lse)
+            p.lse[row0 + gc + lane] = (mt8 + log2f(lt)) * 0.69314718055994531f;
+        }
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int g = gc + e;
           float v = __uint_as_float(o[0][e]);
           if constexpr (E4M3)
-            v = (v + (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.0625f) * 0.0625f) * unit;
+            v += (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.0625f) * 0.0625f;
           else
             v += __uint_as_float(o[1][e]);
-          if (g >= ng) continue;
-          const float *lp = lpart + ob * 4 * GB + g;
-          const float lt = (lp[0] + lp[GB]) + (lp[2 * GB] + lp[3 * GB]);
-          if (starts && ends) {
-            if (f < D) p.o[(row0 + g) * D + f] = static_cast<uint16_t>(pack_bf16(v / lt, 0.f));
-            if (f == 0 && p.lse) p.lse[row0 + g] = (mstat[ob * GB + g] + log2f(lt)) * 0.69314718055994531f;
-          } else {
-            if (f < D) p.part_o[(static_cast<long long>(slot) * GB + g) * D + f] = v;
-            if (f == 0) p.part_ml[slot * GB + g] = make_float2(mstat[ob * GB + g], lt);
+          v *= __shfl_sync(0xffffffffu, mul, e);
+          if (f < D && gc + e < ng) {
+            if (whole)
+              p.o[(row0 + gc + e) * D + f] = static_cast<uint16_t>(pack_bf16(v, 0.f));
+            else
+              p.part_o[(static_cast<long long>(slot) * GB + gc + e) * D + f] = v;
           }
         }
       }
@@ -893,14 +1007,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       wk.advance(p, run);
     }
-    if (threadIdx.x == 128) p.meta[blockIdx.x] = mt;
+    if (warp == C::kEpilogue && lane == 0) p.meta[blockIdx.x] = mt;
     __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kDecIssuer) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == C::kIssuer) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 // Joins the parts of one item for query head blockIdx.y of its block: CTA c's item starts
@@ -920,17 +1034,21 @@ __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __gr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto slot = [&](int i) { return i == 0 ? 2 * static_cast<int>(blockIdx.x) + 1 : 2 * (static_cast<int>(blockIdx.x) + i); };
   // Weights 2^(m_i - M) of the parts, and the total of l.
-  const float2 ml = tid < mt.z ? p.part_ml[slot(tid) * GB + g] : make_float2(-INFINITY, 0.f);
-  float M = ml.x;
+  float M = -INFINITY;
+  for (int i = tid; i < mt.z; i += kJoinThreads) M = fmaxf(M, p.part_ml[slot(i) * GB + g].x);
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) red[warp] = M;
   __syncthreads();
   M = red[0];
   for (int w = 1; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
   __syncthreads();
-  const float w0 = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-  if (tid < mt.z) wgt[tid] = w0;
-  float L = w0 * ml.y;
+  float L = 0.f;
+  for (int i = tid; i < mt.z; i += kJoinThreads) {
+    const float2 ml = p.part_ml[slot(i) * GB + g];
+    const float w = ex2(ml.x - M);
+    wgt[i] = w;
+    L += w * ml.y;
+  }
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   if (lane == 0) red[warp] = L;
   __syncthreads();

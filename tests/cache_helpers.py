@@ -95,11 +95,13 @@ def decode_exact(c: Cache, q, scale, window=0, lens=None):
     The bounds, from the kernel's arithmetic:
     * s sums d products in fp32: |ds| <= g * scale * sum|q k|, g = 2 (d + 2) 2^-24 with
       room for an accumulator that truncates; e4m3 keys take q in two parts whose
-      remainder is at most 2^-20 max|q| per element;
+      remainder is at most 2^-20 max|q| per element, the maximum over the heads that
+      share a cache head (they may share a scale);
     * a weight exp(s - lse) then moves by a factor within exp(+-2 max|ds|); the hardware
       exponential adds 2^-21, q's scale in the log2 domain 2^-22 |s|;
-    * weights go into the product with 16 or more significant bits (2^-16), those of e4m3
-      values not below 2^-22 of the largest value, and the sums over n keys are in fp32.
+    * weights go into the product with 16 significant bits (2^-16); for e4m3 values with
+      fp16's 11 (2^-11, and 2^-12 for the remainder of three e4m3 parts: 2^-10 holds both)
+      and not below 2^-22 of the largest value; the sums over n keys are in fp32.
     """
     B, Hq, d = q.shape
     G = Hq // c.H
@@ -121,10 +123,10 @@ def decode_exact(c: Cache, q, scale, window=0, lens=None):
         lse[b] = z.reshape(Hq)
         ds = 2 * (d + 2) * 2.0 ** -24 * scale * torch.matmul(qb.abs(), K.abs().transpose(1, 2))
         if c.e4m3:
-            ds = ds + 2.0 ** -20 * scale * qb.abs().amax(-1, keepdim=True) * K.abs().sum(-1)[:, None]
+            ds = ds + 2.0 ** -20 * scale * qb.abs().amax((1, 2), keepdim=True) * K.abs().sum(-1)[:, None]
         e = ds.amax(-1) + 2.0 ** -22 * s.abs().amax(-1) + 2.0 ** -21
         sums = m * 2.0 ** -23
-        do[b] = ((torch.expm1(2 * e) + 2.0 ** -16 + sums)[..., None] * torch.matmul(p, V.abs())).reshape(Hq, d)
+        do[b] = ((torch.expm1(2 * e) + 2.0 ** (-10 if c.e4m3 else -16) + sums)[..., None] * torch.matmul(p, V.abs())).reshape(Hq, d)
         if c.e4m3:
             do[b] += (m * 2.0 ** -22 * V.abs().amax((1, 2))[:, None]).expand(c.H, G).reshape(Hq, 1)
         dl[b] = (e + sums + 2.0 ** -22 * z.abs()).reshape(Hq)

@@ -6,11 +6,12 @@ A CTA's share is a list of segments (runs of tiles with one Q).  Roles, as in th
   * issuer: S(n+1) ahead of O += V_n P_n, across segments; slots, Q, P and O are handed
     back by commits;
   * Q warp: the rows of segment i into buffer i % 2;
-  * scales warp (e4m3): the keys' factors of tile n into an 8-slot ring;
-  * softmax, four warps with a vote per tile: read S(n), rewrite the masked rows of V(n)
+  * scales warp (e4m3): the keys' factors of tile n into a 4-slot ring;
+  * softmax, groups of four warps with a vote per tile and group: read S(n), rewrite the masked rows of V(n)
     in a segment's last tile, rescale O when the reference moves (any tile but a
     segment's first), write P(n); the segment's statistics;
   * epilogue, four warps: O and the statistics of a segment.
+Tensor memory lanes: softmax warp w of a group works on the lanes that epilogue warp w reads.
 Checked: no deadlock or phase aliasing; every MMA reads the tiles, the Q, the masked V
 and the P it should; O holds the segment's tiles in order when it is rescaled and when the
 epilogue reads it; no load or write lands in a buffer that is still in use.
@@ -25,11 +26,12 @@ import pytest
 
 from pipeline_model import Bar, Machine
 
-WARPS, SCALES = 4, 8
+GROUP, SCALES = 4, 4
 
 
-def decode_model(runs, slots: int, seed: int, e4m3: bool, skip: str = "") -> None:
+def decode_model(runs, slots: int, seed: int, e4m3: bool, groups: int = 1, skip: str = "") -> None:
     M = Machine(seed)
+    WARPS = GROUP * groups
     rnd = random.Random(seed * 7 + 1)
     total = sum(runs)
     segs, n = [], 0  # (segment, first tile, run)
@@ -40,7 +42,7 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, skip: str = "") -> Non
     first = {n0 for _, n0, _ in segs}
     last = {n0 + r - 1 for _, n0, r in segs}
     partial = {t for t in last if rnd.random() < 0.7} | {t for t in first if rnd.random() < 0.2}
-    moves = {t for t in range(total) if t not in first and rnd.random() < 0.3}
+    moves = [{t for t in range(total) if t not in first and rnd.random() < 0.3} for _ in range(groups)]
 
     full = [Bar(f"full{s}", 1) for s in range(slots)]
     empty = [Bar(f"empty{s}", 1) for s in range(slots)]
@@ -48,10 +50,10 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, skip: str = "") -> Non
     q, q_empty = pair("q", 1), pair("q_empty", 1 + (WARPS if e4m3 else 0))
     s_full, s_empty = pair("s", 1), pair("s_empty", WARPS)
     p_full, p_empty = pair("p", WARPS), pair("p_empty", 1)
-    o_full, o_empty, stat = pair("o", 1), pair("o_empty", WARPS), pair("stat", WARPS)
+    o_full, o_empty, stat = pair("o", 1), pair("o_empty", 4), pair("stat", WARPS)
     sc = [Bar(f"sc{s}", 1) for s in range(SCALES)]
     sc_empty = [Bar(f"sc_empty{s}", WARPS) for s in range(SCALES)]
-    vote = Bar("vote", WARPS)  # bar.red among the softmax warps, one phase per use
+    vote = [Bar(f"vote{g}", GROUP) for g in range(groups)]  # bar.red among a group's warps, one phase per use
 
     def slot(kv, t):
         g = 2 * t + kv
@@ -123,14 +125,14 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, skip: str = "") -> Non
         yield lambda: True
 
     def softmax(w):
-        votes = 0
+        votes, grp = 0, w // GROUP
 
         def agree():
             nonlocal votes
-            vote.arrive()
+            vote[grp].arrive()
             k = votes
             votes += 1
-            yield lambda: vote.done >= k + 1
+            yield lambda: vote[grp].done >= k + 1
 
         for i, n0, r in segs:
             ob = i & 1
@@ -145,7 +147,7 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, skip: str = "") -> Non
                     yield lambda t=t: sc[t % SCALES].ready(t // SCALES)
                     M.read(("sc", t % SCALES), ("sc", t))
                     sc_empty[t % SCALES].arrive()
-                if t in partial:
+                if t in partial and grp == 0:
                     s, ph = slot(1, t)
                     yield lambda s=s, ph=ph: full[s].ready(ph)
                     M.write(("slot", s), v_tag(t))  # each warp its own rows
@@ -154,10 +156,10 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, skip: str = "") -> Non
                 s_empty[b].arrive()
                 if t not in first:
                     yield from agree()
-                if t in first or t in moves:
+                if t in first or t in moves[grp]:
                     M.write(("x", (votes >> 1) & 3, w), t)
                     yield from agree()
-                if t in moves:
+                if t in moves[grp]:
                     if skip != "rescale":
                         yield lambda t=t: p_empty[(t - 1) & 1].ready((t - 1) >> 1)
                     M.read(("O", ob, w), ("O", i, t))
@@ -179,21 +181,22 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, skip: str = "") -> Non
             yield lambda: o_full[ob].ready(i >> 1)
             for x in range(WARPS):
                 M.read(("stat", ob, x), ("stat", i))
-            M.read(("O", ob, w), ("O", i, n0 + r))
+            for g in range(groups):
+                M.read(("O", ob, w + GROUP * g), ("O", i, n0 + r))
             yield lambda: True
             o_empty[ob].arrive()
 
     M.run([producer(), issuer(), q_warp(), scales(), *(softmax(w) for w in range(WARPS)),
-           *(epilogue(w) for w in range(WARPS))])
+           *(epilogue(w) for w in range(4))])
     assert all(o_empty[b].done == (len(runs) + 1 - b) // 2 for b in range(2))
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("slots", [4, 5, 6, 11, 24])
+@pytest.mark.parametrize("slots,groups", [(3, 1), (6, 1), (12, 1), (5, 2), (6, 2), (11, 4)])
 @pytest.mark.parametrize("runs", [[1], [2], [9], [1, 1, 1, 1, 1], [3, 1, 2], [1, 4, 1, 1, 2, 5]])
-def test_pipeline_under_random_interleavings(runs, slots, e4m3):
-    for seed in range(25):
-        decode_model(runs, slots, seed, e4m3)
+def test_pipeline_under_random_interleavings(runs, slots, groups, e4m3):
+    for seed in range(40 // (groups + 1)):
+        decode_model(runs, slots, seed, e4m3, groups)
 
 
 @pytest.mark.parametrize("skip", ["p", "o_empty", "rescale"])
@@ -211,4 +214,4 @@ def test_model_matches_the_kernel():
     """The rings this model runs are the kernel's (read from its source)."""
     src = open(os.path.join(os.path.dirname(__file__), "..", "io_aware_exact_23_b200", "csrc", "fa_decode.cuh")).read()
     assert int(re.search(r"kScStages = (\d+);", src).group(1)) == SCALES
-    assert "kSlots >= 4" in src and "> 24 ? 24" in src
+    assert "kSlots >= 3" in src and "> 24 ? 24" in src
