@@ -28,7 +28,8 @@ struct CacheView {
   const int *seq_lens;
   long long bt_stride;
   int num_pages, H, page_size, B, max_pages;
-  int page_shift;  // log2(page_size), or -1
+  int page_shift;  // log2(page_size), or -1: then page_size is a multiple of 128
+  unsigned long long page_magic;  // ceil(2^64 / (page_size / 128)), where page_shift is -1
   int *status;
   int seq;
 };
@@ -56,16 +57,17 @@ __device__ __forceinline__ int cache_len(const CacheView &c, int b, int kernel) 
   return n;
 }
 
+// The index of position `pos`'s page in its sequence: pos / page_size.  floor(t / k) is the
+// high word of t * ceil(2^64 / k) for every t < 2^32.
+__device__ __forceinline__ int cache_page_index(const CacheView &c, int pos) {
+  if (c.page_shift >= 0) return pos >> c.page_shift;
+  return static_cast<int>(__umul64hi(static_cast<unsigned long long>(pos >> 7), c.page_magic));
+}
+
 // Page and row of position `pos` of sequence b; -1 (and a record) for a bad page id.
 __device__ __forceinline__ int cache_page(const CacheView &c, int b, int pos, int &row, int kernel) {
-  int pi;
-  if (c.page_shift >= 0) {
-    pi = pos >> c.page_shift;
-    row = pos & (c.page_size - 1);
-  } else {
-    pi = pos / c.page_size;
-    row = pos - pi * c.page_size;
-  }
+  const int pi = cache_page_index(c, pos);
+  row = pos - pi * c.page_size;
   const int page = __ldg(c.block_table + b * c.bt_stride + pi);
   if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) {
     record_cache_error(c.status, kernel, b, c.seq);

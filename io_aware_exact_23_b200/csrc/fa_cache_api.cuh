@@ -74,6 +74,7 @@ int make_view(const fa_paged_cache *c, fa::CacheView *v, DeviceState **ds) {
   v->page_shift = -1;
   for (int s = 4; s < 31; ++s)
     if (c->page_size == (1 << s)) v->page_shift = s;
+  v->page_magic = v->page_shift >= 0 ? 0 : ~0ull / static_cast<unsigned>(c->page_size / 128) + 1;
   v->status = (*ds)->status;
   v->seq = next_seq();
   return FA_OK;
@@ -270,6 +271,14 @@ int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, i
   p.nblk = nblk;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.vec_scales = 0;
+  if (cache->type == FA_CACHE_E4M3) {
+    const long long *ks = cache->k_scale_stride, *vs = cache->v_scale_stride;
+    const int extent[2] = {cache->num_pages, cache->H};
+    bool vec = ks[2] == 1 && vs[2] == 1 && aligned16(cache->k_scale) && aligned16(cache->v_scale);
+    for (int a = 0; a < 2; ++a) vec = vec && (extent[a] == 1 || (ks[a] % 4 == 0 && vs[a] % 4 == 0));
+    p.vec_scales = vec;
+  }
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   p.meta = reinterpret_cast<int4 *>(ws);
   p.part_ml = reinterpret_cast<float2 *>(ws + decode_ml_offset());

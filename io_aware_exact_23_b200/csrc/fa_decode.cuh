@@ -51,8 +51,9 @@ struct DecodeParams {
   int Hq, G;          // query heads, and query heads per cache head
   int nblk;           // blocks of GB query heads per cache head
   int window;         // 0: all positions
+  int vec_scales;     // e4m3: four neighbouring tokens' factors are one aligned 16-byte piece
   float scale_log2;   // scale * log2(e)
-  int4 *meta;         // [kDecodeMaxCtas] item whose parts start at CTA c: {b, item, parts, -}; parts 0: none
+  int4 *meta;         // [kDecodeMaxCtas] item whose parts start at CTA c: {b, first query head, parts, -}; parts 0: none
   float2 *part_ml;    // [2 * kDecodeMaxCtas][GB] (m, l) of a part
   float *part_o;      // [2 * kDecodeMaxCtas][GB][d]
 };
@@ -204,9 +205,12 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool mine) {
   return r != 0;
 }
 
-// 4-byte asynchronous copy global -> shared; zeros if !valid.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+// 4- and 16-byte asynchronous copies global -> shared.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const float *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // Arrive on `bar` once this thread's earlier cp.async copies have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
@@ -232,32 +236,60 @@ __device__ __forceinline__ void reduce_columns(float (&v)[N], F f) {
   for (; bit >= 1; bit >>= 1) v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
 }
 
+// `total` tiles dealt out to `nc` CTAs, the first of them one more where it does not divide.
+struct DecodeSplit {
+  int q, r;
+  __device__ __forceinline__ DecodeSplit(int total, int nc) : q(total / nc), r(total % nc) {}
+  __device__ __forceinline__ int begin(int c) const { return q * c + min(c, r); }
+  __device__ __forceinline__ int owner(int tile) const {
+    const int wide = r * (q + 1);
+    return tile < wide ? tile / (q + 1) : r + (tile - wide) / q;
+  }
+};
+
+// The next sequence after b with a tile (-1: none), from the 32 lengths held from `base` on
+// and then further ones.  Out of line: it is rare, and instruction fetch is scarce.
+struct DecodeNext {
+  int b, base, lane_len;
+};
+__device__ __noinline__ DecodeNext decode_next(const DecodeParams &p, int b, int base, int lane_len) {
+  for (;;) {
+    const uint32_t later = __ballot_sync(0xffffffffu, lane_len > 0 && base + static_cast<int>(lane_id()) > b);
+    if (later) return {base + __ffs(later) - 1, base, lane_len};
+    base += 32;
+    if (base >= p.c.B) return {-1, base, 0};
+    const int i = base + static_cast<int>(lane_id());
+    lane_len = i < p.c.B ? cache_len(p.c, i, kKernelDecode) : 0;
+  }
+}
+
 // A walk over this CTA's tiles, run by a whole warp.  Lane i holds the length of sequence
 // base + i, so that moving on to another sequence costs a load once in 32.
 struct DecodeWalk {
-  int b, x, off, rem;        // sequence, item of it, tile of the item, tiles left to this CTA
+  int b, h, blk, off, rem;   // sequence, cache head, block of query heads, tile of the item, tiles left to this CTA
   int len, first, tile0, n;  // b's length, first visible position, its tile, and the item's tiles
   int base, lane_len;
 
-  __device__ __forceinline__ void window32(const DecodeParams &p, int at) {
-    base = at;
-    const int i = at + static_cast<int>(lane_id());
-    lane_len = i < p.c.B ? cache_len(p.c, i, kKernelDecode) : 0;
+  __device__ __forceinline__ static int first_of(const DecodeParams &p, int len) {
+    return p.window > 0 ? max(0, len - p.window) : 0;
   }
   __device__ __forceinline__ void sequence(const DecodeParams &p) {
     len = __shfl_sync(0xffffffffu, lane_len, b - base);
-    first = p.window > 0 ? max(0, len - p.window) : 0;
+    first = first_of(p, len);
     tile0 = first >> 7;
     n = ((len + 127) >> 7) - tile0;
   }
-  __device__ __forceinline__ void start(const DecodeParams &p, int b0, int x0, int off0, int tiles) {
-    b = b0;
-    x = x0;
-    off = off0;
-    rem = tiles;
-    base = lane_len = len = first = tile0 = n = 0;
+  __device__ __forceinline__ void start(const DecodeParams &p, const int *share) {
+    h = share[1];
+    blk = share[6];
+    off = share[2];
+    rem = share[3];
+    b = base = lane_len = len = first = tile0 = n = 0;
     if (rem > 0) {
-      window32(p, b);
+      const DecodeNext nx = decode_next(p, share[0] - 1, share[0] - 32, 0);
+      b = nx.b;
+      base = nx.base;
+      lane_len = nx.lane_len;
       sequence(p);
     }
   }
@@ -269,22 +301,70 @@ struct DecodeWalk {
     off += k;
     if (rem <= 0 || off < n) return;
     off = 0;
-    if (++x < p.c.H * p.nblk) return;
-    x = 0;
-    for (;;) {
-      const uint32_t later = __ballot_sync(0xffffffffu, lane_len > 0 && base + static_cast<int>(lane_id()) > b);
-      if (later) {
-        b = base + __ffs(later) - 1;
-        break;
-      }
-      if (base + 32 >= p.c.B) {  // not reached while tiles are left
-        rem = 0;
-        return;
-      }
-      b = base + 31;
-      window32(p, base + 32);
+    if (++blk < p.nblk) return;
+    blk = 0;
+    if (++h < p.c.H) return;
+    h = 0;
+    const DecodeNext nx = decode_next(p, b, base, lane_len);
+    if (nx.b < 0) {  // not reached while tiles are left
+      rem = 0;
+      return;
     }
+    b = nx.b;
+    base = nx.base;
+    lane_len = nx.lane_len;
     sequence(p);
+  }
+};
+
+// The page ids of the walk's position, 32 at a time (lane i: page 32 * blk + i of sequence b),
+// with the next 32 that will be asked for already on their way.  An id is -1 where the
+// sequence needs no page and num_pages where the table is out of range.
+struct DecodePages {
+  int b = -1, blk = -1, ids = -1;
+  int nb = -1, nblk = -1, nids = -1;
+
+  __device__ __forceinline__ static int load(const CacheView &c, int b, int blk, int len, int first) {
+    const int i = 32 * blk + static_cast<int>(lane_id());
+    return i >= cache_page_index(c, first) && i <= cache_page_index(c, len - 1) ? __ldg(c.block_table + b * c.bt_stride + i) : -1;
+  }
+  // To the pages of the walk's tile, which begins at position pos0; returns its first page.
+  __device__ __forceinline__ int seek(const DecodeParams &p, const DecodeWalk &wk, int pos0) {
+    const CacheView &c = p.c;
+    const int pi = cache_page_index(c, pos0), at = pi >> 5;
+    if (wk.b == b && at == blk) return pi;
+    int id = wk.b == nb && at == nblk ? nids : load(c, wk.b, at, wk.len, wk.first);
+    b = wk.b;
+    blk = at;
+    if (id >= c.num_pages || id < -1 || (id == -1 && load_needed(c, wk, at))) {
+      record_cache_error(c.status, kKernelDecode, b, c.seq);
+      id = c.num_pages;
+    }
+    ids = id;
+    // What comes next: the sequence's next block, its first one for the next head, or the
+    // next sequence's first (as far as the walk holds its length).
+    const int home = cache_page_index(c, wk.tile0 << 7) >> 5;
+    nb = -1;
+    if (at < (cache_page_index(c, wk.len - 1) >> 5) || (wk.h + 1 < c.H && home != at)) {
+      nb = b;
+      nblk = at < (cache_page_index(c, wk.len - 1) >> 5) ? at + 1 : home;
+      nids = load(c, nb, nblk, wk.len, wk.first);
+    } else {
+      const uint32_t later =
+          __ballot_sync(0xffffffffu, wk.lane_len > 0 && wk.base + static_cast<int>(lane_id()) > b);
+      if (later) {
+        nb = wk.base + __ffs(later) - 1;
+        const int len = __shfl_sync(0xffffffffu, wk.lane_len, nb - wk.base);
+        const int first = DecodeWalk::first_of(p, len);
+        nblk = cache_page_index(c, first & ~127) >> 5;
+        nids = load(c, nb, nblk, len, first);
+      }
+    }
+    return pi;
+  }
+  __device__ __forceinline__ static bool load_needed(const CacheView &c, const DecodeWalk &wk, int at) {
+    const int i = 32 * at + static_cast<int>(lane_id());
+    return i >= cache_page_index(c, wk.first) && i <= cache_page_index(c, wk.len - 1);
   }
 };
 
@@ -310,7 +390,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   int *words = reinterpret_cast<int *>(bars + C::kFixedBars);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(words);
   volatile int *abort_flag = words + 1;
-  int *share = words + 2;  // b, x, off, tiles of this CTA's share, then T, nc and "do nothing"
+  int *share = words + 2;  // first sequence, head, tile and the number of tiles, T, nc, block of heads, "do nothing"
   uint64_t *bar_full = reinterpret_cast<uint64_t *>(words + 12);  // [kSlots]
   uint64_t *bar_empty = bar_full + C::kSlots;                     // [kSlots]
   float *xmax = reinterpret_cast<float *>(smem + C::kMiscOff);    // [2][GB][4]
@@ -328,38 +408,41 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   // The join kernel may be put on the SMs' leftovers now; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < 7; ++i) share[i] = 0;
-    if ((smem_u32(smem) & 1023u) != 0) {
-      record_failure(ctx, kStatusInternal, 0);
-      share[6] = 1;
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_q[i], 32);
+  if (warp == 0) {
+    if (lane < 2) {
+      mbar_init(&bar_q[lane], 32);
       // The issuer's commit; e4m3: and the softmax warps, for q's scale.
-      mbar_init(&bar_q_empty[i], 1 + (E4M3 ? C::kSoftmaxWarps : 0));
-      mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_s_empty[i], C::kSoftmaxWarps);
-      mbar_init(&bar_p[i], C::kSoftmaxWarps);
-      mbar_init(&bar_p_empty[i], 1);
-      mbar_init(&bar_o[i], 1);
-      mbar_init(&bar_o_empty[i], 4);
-      mbar_init(&bar_stat[i], C::kSoftmaxWarps);
+      mbar_init(&bar_q_empty[lane], 1 + (E4M3 ? C::kSoftmaxWarps : 0));
+      mbar_init(&bar_s[lane], 1);
+      mbar_init(&bar_s_empty[lane], C::kSoftmaxWarps);
+      mbar_init(&bar_p[lane], C::kSoftmaxWarps);
+      mbar_init(&bar_p_empty[lane], 1);
+      mbar_init(&bar_o[lane], 1);
+      mbar_init(&bar_o_empty[lane], 4);
+      mbar_init(&bar_stat[lane], C::kSoftmaxWarps);
     }
-    mbar_init(bar_drain, 1);
-    for (int i = 0; i < C::kScStages; ++i) {
-      mbar_init(&bar_sc[i], 32);
-      mbar_init(&bar_sc_empty[i], C::kSoftmaxWarps);
+    if (lane < C::kScStages) {
+      mbar_init(&bar_sc[lane], 32);
+      mbar_init(&bar_sc_empty[lane], C::kSoftmaxWarps);
     }
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&bar_full[i], 1);
-      mbar_init(&bar_empty[i], 1);
+    if (lane < C::kSlots) {
+      mbar_init(&bar_full[lane], 1);
+      mbar_init(&bar_empty[lane], 1);
+    }
+    if (lane < 8) share[lane] = 0;
+    __syncwarp();
+    if (lane == 0) {
+      mbar_init(bar_drain, 1);
+      *abort_flag = 0;
+      if ((smem_u32(smem) & 1023u) != 0) {
+        record_failure(ctx, kStatusInternal, 0);
+        share[7] = 1;
+      }
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
     }
     fence_barrier_init();
     fence_proxy_async_smem();
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
   }
   if (warp == C::kIssuer) {
     tmem_alloc(tmem_slot, C::kTmemCols);
@@ -379,6 +462,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       return ((len + 127) >> 7) - (first >> 7);
     };
     int mine = 0;
+#pragma unroll 1
     for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(b) * items;
     int incl = mine;
 #pragma unroll
@@ -395,24 +479,27 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       if (w < warp) before += sums[w];
       total += sums[w];
     }
-    const int nc = min(static_cast<int>(gridDim.x), total);
-    if (static_cast<int>(blockIdx.x) < nc) {
-      const int t0 = static_cast<int>(static_cast<long long>(total) * blockIdx.x / nc);
-      const int t1 = static_cast<int>(static_cast<long long>(total) * (blockIdx.x + 1) / nc);
+    const int nc = min(static_cast<int>(gridDim.x), total), c = static_cast<int>(blockIdx.x);
+    if (c < nc) {
+      const DecodeSplit sp(total, nc);
+      const int t0 = sp.begin(c);
       const int excl = before + incl - mine;
       if (mine > 0 && t0 >= excl && t0 < excl + mine) {
         int b = b_lo, at = t0 - excl;
         int n = tiles_of(b);
+#pragma unroll 1
         while (at >= n * items) {
           at -= n * items;
           n = tiles_of(++b);
         }
         share[0] = b;
-        share[1] = at / n;
+        const int item = at / n;
+        share[1] = item / p.nblk;
         share[2] = at % n;
-        share[3] = t1 - t0;
+        share[3] = share[7] ? 0 : sp.begin(c + 1) - t0;
         share[4] = total;
         share[5] = nc;
+        share[6] = item % p.nblk;
       }
     }
   }
@@ -423,52 +510,45 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   constexpr uint32_t kOCol0 = 2 * C::kQCols;
 
   DecodeWalk wk;
-  wk.start(p, share[0], share[1], share[2], share[6] ? 0 : share[3]);
+  wk.start(p, share);
 
   if (warp == C::kProducer) {
     // ------------------------------------------------------------- producer
-    // Lane i loads page i of a tile (pages of 128 rows or more: lane 0 alone).  The page
-    // ids of the next tile are read while this tile's slots are waited for.
+    // Lane i loads page i of a tile (pages of 128 rows or more: lane 0 alone).
     const int rows = min(p.c.page_size, 128);
     const int pages = 128 / rows;
-    auto page_of = [&](bool &need) {
-      const int pos = (wk.tile0 + wk.off) * 128 + lane * rows;
-      need = wk.rem > 0 && lane < pages && pos < wk.len && pos + rows > wk.first;
-      int row = 0, page = 0;
-      if (need) {
-        page = cache_page(p.c, wk.b, pos, row, kKernelDecode);
-        if (page < 0) page = p.c.num_pages;  // out of the tensor map's range: TMA fills with zeros
-      }
-      return make_int2(page, row);
-    };
-    bool need, ok = true;
-    int2 at = page_of(need);
+    DecodePages pg;
+    bool ok = true;
     int g = 0, s = 0;        // slots filled so far, and the next one
     uint32_t ph = 1;         // its "empty" phase: the first round passes at once
     while (wk.rem > 0 && ok) {
-      const int h = wk.x / p.nblk;
+      const int pos0 = (wk.tile0 + wk.off) << 7;
+      const int pi = pg.seek(p, wk, pos0);
+      // A page out of the table's range is out of the tensor map's: TMA fills with zeros.
+      const int page = __shfl_sync(0xffffffffu, pg.ids, (pi + lane) & 31);
+      const bool need = lane < pages && page >= 0;
+      const int row = pages == 1 ? pos0 - pi * p.c.page_size : 0;
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, need)) * rows * C::kRowBytes;
-      const bool now = need;
-      const int2 here = at;
-      wk.advance(p, 1);
-      at = page_of(need);
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++g) {
         if (!(ok = __all_sync(0xffffffffu, decode_wait(ctx, &bar_empty[s], ph, kTagDEmpty)))) break;
         if (lane == 0) mbar_arrive_expect_tx(&bar_full[s], bytes);
         __syncwarp();
-        if (now)
+        if (need)
           for (int i = 0; i < C::kPanels; ++i)
             tma_load_4d(kv == 0 ? &tmK : &tmV, &bar_full[s],
                         ring + s * C::kTileBytes + i * C::kPanelBytes + lane * rows * C::kPanelRow,
-                        i * (C::kPanelRow / C::kElem), here.y, h, here.x);
+                        i * (C::kPanelRow / C::kElem), row, wk.h, page);
         __syncwarp();
         if (++s == C::kSlots) {
           s = 0;
           ph ^= 1;
         }
       }
+      wk.advance(p, 1);
     }
     // The last loads have landed before the CTA can exit.
+#pragma unroll 1
     for (int i = 0; i < C::kSlots && i < g; ++i) mbar_drain(&bar_full[i], ((g - 1 - i) / C::kSlots) & 1);
     __syncwarp();
   } else if (warp == C::kIssuer) {
@@ -501,38 +581,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         ph ^= 1;
       }
     };
-    int n = 0;  // tiles whose S^T was issued
-    // What V^T P of the previous tile needs to know.
-    bool pend = false, pend_first = false, pend_last = false;
-    int pend_seg = 0, pend_s = 0;
+    // The previous tile's segment, place in it and V slot (seg -1: no tile yet).
+    int seg = 0, pend_seg = -1, pend_s = 0;
     uint32_t pend_ph = 0;
-    auto issue_o = [&](int i) {  // tile i's V^T P
-      const int buf = i & 1, ob = pend_seg & 1;
-      if (pend_first && pend_seg >= 2 && !wait(&bar_o_empty[ob], ((pend_seg >> 1) - 1) & 1, kTagDOEmpty)) return false;
-      if (!wait(&bar_full[pend_s], pend_ph, kTagDFull)) return false;
-      if (!wait(&bar_p[buf], (i >> 1) & 1, kTagDP)) return false;
-      tc_fence_after();
-      const uint64_t vd = sdesc_add(v_desc0, pend_s * C::kTileBytes), pd = sdesc_add(p_desc0, buf * C::kPBytes);
-      const uint32_t to = tm + kOCol0 + ob * C::kOCols;
-      constexpr int kStep = E4M3 ? 32 : 16;  // keys per instruction
-#pragma unroll
-      for (int ks = 0; ks < 128 / kStep; ++ks) {
-        const uint64_t a = sdesc_add(vd, ks * kStep * C::kPanelRow), b = sdesc_add(pd, ks * kStep * C::kPRow);
-        if constexpr (E4M3)
-          mma_ss_f8_w(to, a, b, idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
-        else
-          mma_ss_w(to, a, b, idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
-      }
-      mma_commit_w(&bar_empty[pend_s]);
-      mma_commit_w(&bar_p_empty[buf]);
-      if (pend_last) mma_commit_w(&bar_o[ob]);
-      return true;
-    };
-    for (int seg = 0; wk.rem > 0 && ok; ++seg) {
-      const int run = wk.run(), qb = seg & 1;
-      if (!(ok = wait(&bar_q[qb], (seg >> 1) & 1, kTagDQ))) break;
-      for (int i = 0; i < run && ok; ++i, ++n) {
-        const int buf = n & 1;
+    bool begins = true, pend_first = false, pend_last = false;
+    for (int n = 0;; ++n) {
+      const int buf = n & 1, qb = seg & 1;
+      const bool more = wk.rem > 0, ends = wk.run() == 1;
+      if (more) {
+        if (begins && !(ok = wait(&bar_q[qb], (seg >> 1) & 1, kTagDQ))) break;
         if (n >= 2 && !(ok = wait(&bar_s_empty[buf], ((n >> 1) - 1) & 1, kTagDSEmpty))) break;
         if (!(ok = wait(&bar_full[s], ph, kTagDFull))) break;
         tc_fence_after();
@@ -549,20 +606,41 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         }
         mma_commit_w(&bar_empty[s]);
         mma_commit_w(&bar_s[buf]);
-        if (i + 1 == run) mma_commit_w(&bar_q_empty[qb]);
-        if (pend && !(ok = issue_o(n - 1))) break;
-        pend = true;
-        pend_first = i == 0;
-        pend_last = i + 1 == run;
-        pend_seg = seg;
-        next_slot();
-        pend_s = s;
-        pend_ph = ph;
-        next_slot();
+        if (ends) mma_commit_w(&bar_q_empty[qb]);
       }
-      if (ok) wk.advance(p, run);
+      if (pend_seg >= 0) {  // V^T P of tile n - 1
+        const int pb = buf ^ 1, ob = pend_seg & 1;
+        if (pend_first && pend_seg >= 2 && !(ok = wait(&bar_o_empty[ob], ((pend_seg >> 1) - 1) & 1, kTagDOEmpty))) break;
+        if (!(ok = wait(&bar_full[pend_s], pend_ph, kTagDFull))) break;
+        if (!(ok = wait(&bar_p[pb], ((n - 1) >> 1) & 1, kTagDP))) break;
+        tc_fence_after();
+        const uint64_t vd = sdesc_add(v_desc0, pend_s * C::kTileBytes), pd = sdesc_add(p_desc0, pb * C::kPBytes);
+        const uint32_t to = tm + kOCol0 + ob * C::kOCols;
+        constexpr int kStep = E4M3 ? 32 : 16;  // keys per instruction
+#pragma unroll
+        for (int ks = 0; ks < 128 / kStep; ++ks) {
+          const uint64_t a = sdesc_add(vd, ks * kStep * C::kPanelRow), b = sdesc_add(pd, ks * kStep * C::kPRow);
+          if constexpr (E4M3)
+            mma_ss_f8_w(to, a, b, idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
+          else
+            mma_ss_w(to, a, b, idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
+        }
+        mma_commit_w(&bar_empty[pend_s]);
+        mma_commit_w(&bar_p_empty[pb]);
+        if (pend_last) mma_commit_w(&bar_o[ob]);
+      }
+      if (!more) break;
+      pend_seg = seg;
+      pend_first = begins;
+      pend_last = ends;
+      begins = ends;
+      seg += ends ? 1 : 0;
+      next_slot();
+      pend_s = s;
+      pend_ph = ph;
+      next_slot();
+      wk.advance(p, 1);
     }
-    if (ok && pend) ok = issue_o(n - 1);
     if (!ok) {
       mma_commit_w(bar_drain);
       mbar_drain(bar_drain, 0);
@@ -571,18 +649,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   } else if (warp == C::kQWarp) {
     // ---------------------------------------------------------------- Q rows
     // Rows of the segment's query heads into swizzled shared memory, 8 at a time; the next
-    // 8 (of this segment or the next) are read meanwhile.  Rows past the last head are 0.
-    constexpr int kWords = D / 64;  // 32-bit words (2 elements) of a row per lane
-    uint32_t w[8][kWords];
+    // 8 (of this segment or the next) are read meanwhile.  Lane's piece i is 16 bytes, the
+    // (32 i + lane)th of the 8 rows.  Rows past the last head are 0.
+    constexpr int kPieces = D / 32, kPerRow = D / 8;
+    uint4 w[kPieces];
     auto load = [&](int c) {
-      const int h = wk.x / p.nblk, g0 = (wk.x % p.nblk) * GB + 8 * c;
-      const uint32_t *src = reinterpret_cast<const uint32_t *>(
-          p.q + (static_cast<long long>(wk.b) * p.Hq + h * p.G + g0) * D) + lane * kWords;
+      const int g0 = wk.blk * GB + 8 * c;
+      const uint16_t *src = p.q + (static_cast<long long>(wk.b) * p.Hq + wk.h * p.G + g0) * D;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const bool live = wk.rem > 0 && g0 + r < p.G;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) w[r][i] = live ? __ldg(src + r * (D / 2) + i) : 0u;
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = 32 * i + lane;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (wk.rem > 0 && g0 + at / kPerRow < p.G) w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + at);
       }
     };
     bool ok = true;
@@ -591,66 +669,60 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       const int qb = seg & 1;
       if (seg >= 2 && !(ok = __all_sync(0xffffffffu, decode_wait(ctx, &bar_q_empty[qb], ((seg >> 1) - 1) & 1, kTagDQEmpty))))
         break;
-      uint8_t *dst = smem + C::kQOff + qb * C::kQBytes;
+      const uint32_t dst = smem_u32(smem + C::kQOff) + qb * C::kQBytes;
 #pragma unroll 1
       for (int c = 0; c < C::kGroups; ++c) {
-        uint32_t v[8][kWords];
+        uint4 v[kPieces];
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) v[r][i] = w[r][i];
-        if (c + 1 < C::kGroups) {
-          load(c + 1);
-        } else {
-          wk.advance(p, wk.run());
-          load(0);
-        }
+        for (int i = 0; i < kPieces; ++i) v[i] = w[i];
+        if (c + 1 == C::kGroups) wk.advance(p, wk.run());
+        load(c + 1 == C::kGroups ? 0 : c + 1);
         if constexpr (!E4M3) {
-          const int byte = lane * 4 * kWords;  // this lane's elements in the row
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            uint8_t *at = dst + (byte >> 7) * (C::kQRows * 128) + swizzled<128>(8 * c + r, byte & 127);
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t *>(at)[i] = v[r][i];
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = 8 * c + (32 * i + lane) / kPerRow, in = (32 * i + lane) % kPerRow;
+            st_shared_v4(dst + (in >> 3) * (C::kQRows * 128) + swizzled<128>(row, (in & 7) * 16), v[i].x, v[i].y, v[i].z,
+                         v[i].w);
           }
         } else {
           // Scale the 8 rows by the power of two that brings their largest element into
-          // [128, 256), then split: hi = e4m3(x), lo = e4m3(16 (x - hi)).  A row's scores
-          // are off by at most 2^-20 of the group's largest.
-          float m = 0.f;
+          // [128, 256), then split: hi = e4m3(x), lo = e4m3(16 (x - hi)) (bf16 values are
+          // fp16 values in that range).  A row's scores are off by at most 2^-20 of the
+          // group's largest.
+          uint32_t top = 0;
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(v[r][i])), fabsf(bf16_hi(v[r][i]))));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          // m in [2^(e-127), 2^(e-126)); x * 2^(134 - e).  An infinity (e = 255) makes every
-          // score NaN, as a NaN does by itself.
-          const int e0 = static_cast<int>(__float_as_uint(m) >> 23), e = min(max(e0, 16), 250);
+          for (int i = 0; i < kPieces; ++i) {
+            const uint32_t a = __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu);
+            const uint32_t b = __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu);
+            top = __vmaxu2(top, __vmaxu2(a, b));
+          }
+          top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+          // The largest element is in [2^(e-127), 2^(e-126)); x * 2^(134 - e).  An infinity or
+          // NaN (e = 255) makes every score of the group NaN.
+          const int e0 = static_cast<int>(top >> 7), e = min(max(e0, 16), 250);
           const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
           if (lane == 0)
             qscale[qb * C::kGroups + c] =
                 __uint_as_float(e0 == 255 ? 0x7fc00000u : static_cast<uint32_t>(e - 7) << 23) * p.scale_log2;
-          const int byte = lane * 2 * kWords;
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            uint32_t part[2] = {0u, 0u};
+          for (int i = 0; i < kPieces; ++i) {
+            const uint32_t words[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t part[2][2] = {{0u, 0u}, {0u, 0u}};
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-              const float a = bf16_lo(v[r][i]) * up, b = bf16_hi(v[r][i]) * up;
-              const uint32_t h2 = pack_e4m3x4(a, b, 0.f, 0.f);
-              const float2 back = e4m3x2_to_float2(static_cast<uint16_t>(h2));
-              part[0] |= h2 << (16 * i);
-              part[1] |= pack_e4m3x4((a - back.x) * 16.f, (b - back.y) * 16.f, 0.f, 0.f) << (16 * i);
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t r = pack_f16(bf16_lo(words[k]) * up, bf16_hi(words[k]) * up);
+              const uint16_t hi = f16x2_to_e4m3x2(r);
+              const uint16_t lo = f16x2_to_e4m3x2(f16x2_rest(r, e4m3x2_to_f16x2(hi)));
+              part[0][k >> 1] |= static_cast<uint32_t>(hi) << (16 * (k & 1));
+              part[1][k >> 1] |= static_cast<uint32_t>(lo) << (16 * (k & 1));
             }
+            const int row = 8 * c + (32 * i + lane) / kPerRow, byte = (32 * i + lane) % kPerRow * 8;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint8_t *at = dst + swizzled<C::kPanelRow>(k * GB + 8 * c + r, byte);
-              if constexpr (kWords == 2)
-                *reinterpret_cast<uint32_t *>(at) = part[k];
-              else
-                *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(part[k]);
-            }
+            for (int k = 0; k < 2; ++k)
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
+                               dst + swizzled<C::kPanelRow>(k * GB + row, byte & ~15) + (byte & 8)),
+                           "r"(part[k][0]), "r"(part[k][1])
+                           : "memory");
           }
         }
       }
@@ -661,38 +733,40 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   } else if (warp == C::kScales) {
     // ------------------------------------------------- the keys' factors (e4m3)
     if constexpr (E4M3) {
-      // Lane i copies the factors of keys i, i + 32, ... of a tile; the next tile's page
-      // ids are read ahead.
-      int page[4], row[4];
-      auto pages_of = [&]() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int pos = (wk.tile0 + wk.off) * 128 + 32 * i + lane;
-          page[i] = -1;
-          if (wk.rem > 0 && pos >= wk.first && pos < wk.len) page[i] = cache_page(p.c, wk.b, pos, row[i], kKernelDecode);
-        }
-      };
-      pages_of();
+      // A lane copies the factors of keys 4 lane .. 4 lane + 3 at once where they are one
+      // aligned piece (tokens adjacent), else those of keys lane, lane + 32, ...  Keys without
+      // a page are left as they are: the softmax warps mask them.
+      const int rows = min(p.c.page_size, 128), shift = 31 - __clz(rows);
+      DecodePages pg;
       for (int n = 0; wk.rem > 0; ++n) {
         const int st = n % C::kScStages;
+        const int pos0 = (wk.tile0 + wk.off) << 7;
+        const int pi = pg.seek(p, wk, pos0);
+        const int row0 = rows == 128 ? pos0 - pi * p.c.page_size : 0;
         if (n >= C::kScStages &&
             !__all_sync(0xffffffffu, decode_wait(ctx, &bar_sc_empty[st], (n / C::kScStages - 1) & 1, kTagDScEmpty)))
           break;
-        const int h = wk.x / p.nblk;
         const uint32_t dst = smem_u32(smem + C::kScOff) + st * 1024;
+#pragma unroll 1
+        for (int i = 0; i < (p.vec_scales ? 1 : 4); ++i) {
+          const int key = p.vec_scales ? 4 * lane : 32 * i + lane;
+          const int page = __shfl_sync(0xffffffffu, pg.ids, (pi + (key >> shift)) & 31);
+          if (page >= 0 && page < p.c.num_pages) {
+            const int row = row0 + (key & (rows - 1));
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool live = page[i] >= 0;
-            const long long off = live ? page[i] * p.c.scale_stride[kv][0] + h * p.c.scale_stride[kv][1] +
-                                             row[i] * p.c.scale_stride[kv][2]
-                                       : 0;
-            cp_async4(dst + kv * 512 + (32 * i + lane) * 4, p.c.scale[kv] + off, live);
+            for (int kv = 0; kv < 2; ++kv) {
+              const float *src = p.c.scale[kv] + (page * p.c.scale_stride[kv][0] + wk.h * p.c.scale_stride[kv][1] +
+                                                  row * p.c.scale_stride[kv][2]);
+              if (p.vec_scales)
+                cp_async16(dst + kv * 512 + key * 4, src);
+              else
+                cp_async4(dst + kv * 512 + key * 4, src);
+            }
           }
+        }
+        __syncwarp();
         cp_async_arrive(&bar_sc[st]);
         wk.advance(p, 1);
-        pages_of();
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
@@ -938,11 +1012,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     // Thread = feature (tensor memory lane).  Idle sequences first: o = 0, lse = -inf.
     const int f = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+#pragma unroll 1
     for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
       if (cache_len(p.c, b, kKernelDecode) > 0) continue;
       const long long row0 = static_cast<long long>(b) * p.Hq;
+#pragma unroll 1
       for (int e = f; e < p.Hq * D / 8; e += 128) reinterpret_cast<uint4 *>(p.o + row0 * D)[e] = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse)
+#pragma unroll 1
         for (int e = f; e < p.Hq; e += 128) p.lse[row0 + e] = -INFINITY;
     }
     // The item that starts in this CTA's last segment and goes on in the next CTA, if any.
@@ -951,34 +1028,36 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     bool ok = true;
     for (int seg = 0; wk.rem > 0 && ok; ++seg) {
       const int ob = seg & 1, run = wk.run();
-      const int h = wk.x / p.nblk, g0 = (wk.x % p.nblk) * GB, ng = min(GB, p.G - g0);
+      const int g0 = wk.blk * GB, ng = min(GB, p.G - g0);
       const bool starts = wk.off == 0, ends = wk.off + run == wk.n;
       ok = __all_sync(0xffffffffu, decode_wait(ctx, &bar_stat[ob], (seg >> 1) & 1, kTagDStat) &&
                                        decode_wait(ctx, &bar_o[ob], (seg >> 1) & 1, kTagDO));
       if (!ok) break;
       tc_fence_after();
       const uint32_t to = tmem + lane_off + kOCol0 + ob * C::kOCols;
-      const long long row0 = static_cast<long long>(wk.b) * p.Hq + h * p.G + g0;
+      const long long row0 = static_cast<long long>(wk.b) * p.Hq + wk.h * p.G + g0;
       const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
       const bool whole = starts && ends;
 #pragma unroll 1
-      for (int gc = 0; gc < GB; gc += 8) {
+      for (int gc = 0; gc < ng; gc += 8) {
         uint32_t o[C::kOParts][8];
 #pragma unroll
         for (int part = 0; part < C::kOParts; ++part) tmem_ld8(to + part * GB + gc, o[part]);
         // Lane g < 8 has head gc + g's sums.
         const float *lp = lpart + ob * 4 * GB + gc + (lane & 7);
         const float lt = (lp[0] + lp[GB]) + (lp[2 * GB] + lp[3 * GB]);
-        const float mt8 = mstat[ob * GB + gc + (lane & 7)];
+        const float m8 = mstat[ob * GB + gc + (lane & 7)];
         float mul = E4M3 ? vstat[ob * C::kGroups + gc / 8] : 1.f;
-        if (whole) mul /= lt;
+        if (whole) mul = __fdividef(mul, lt);
         if ((warp & 3) == 0 && lane < 8 && gc + lane < ng) {
           if (!whole)
-            p.part_ml[slot * GB + gc + lane] = make_float2(mt8, lt);
+            p.part_ml[slot * GB + gc + lane] = make_float2(m8, lt);
           else if (p.lse)
-            p.lse[row0 + gc + lane] = (mt8 + log2f(lt)) * 0.69314718055994531f;
+            p.lse[row0 + gc + lane] = (m8 + log2f(lt)) * 0.69314718055994531f;
         }
         tmem_wait_ld();
+        uint16_t *po = p.o + (row0 + gc) * D + f;
+        float *pp = p.part_o + (static_cast<long long>(slot) * GB + gc) * D + f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float v = __uint_as_float(o[0][e]);
@@ -989,9 +1068,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           v *= __shfl_sync(0xffffffffu, mul, e);
           if (f < D && gc + e < ng) {
             if (whole)
-              p.o[(row0 + gc + e) * D + f] = static_cast<uint16_t>(pack_bf16(v, 0.f));
+              po[e * D] = static_cast<uint16_t>(pack_bf16(v, 0.f));
             else
-              p.part_o[(static_cast<long long>(slot) * GB + gc + e) * D + f] = v;
+              pp[e * D] = v;
           }
         }
       }
@@ -999,11 +1078,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_o_empty[ob]);
       if (starts && !ends) {
-        // Tile x lies in CTA ceil((x + 1) nc / T) - 1.
-        const int t1 = static_cast<int>(static_cast<long long>(total) * (blockIdx.x + 1) / nc);
-        const long long last = static_cast<long long>(t1) + (wk.n - run) - 1;
-        const int c1 = static_cast<int>(((last + 1) * nc + total - 1) / total) - 1;
-        mt = make_int4(wk.b, wk.x, c1 - static_cast<int>(blockIdx.x) + 1, 0);
+        const DecodeSplit sp(total, nc);
+        const int c = static_cast<int>(blockIdx.x);
+        mt = make_int4(wk.b, wk.h * p.G + g0, sp.owner(sp.begin(c + 1) + (wk.n - run) - 1) - c + 1, 0);
       }
       wk.advance(p, run);
     }
@@ -1029,8 +1106,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __gr
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 mt = p.meta[blockIdx.x];
   const int g = blockIdx.y;
-  const int h = mt.y / p.nblk, g0 = (mt.y % p.nblk) * GB;
-  if (mt.z == 0 || g0 + g >= p.G) return;
+  if (mt.z == 0 || mt.y % p.G + g >= p.G) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto slot = [&](int i) { return i == 0 ? 2 * static_cast<int>(blockIdx.x) + 1 : 2 * (static_cast<int>(blockIdx.x) + i); };
   // Weights 2^(m_i - M) of the parts, and the total of l.
@@ -1061,7 +1137,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __gr
   __syncthreads();
   if (grp != 0) return;
   for (int k = 1; k < kGroups; ++k) acc += part[k][f];
-  const long long row = static_cast<long long>(mt.x) * p.Hq + h * p.G + g0 + g;
+  const long long row = static_cast<long long>(mt.x) * p.Hq + mt.y + g;
   p.o[row * D + f] = static_cast<uint16_t>(pack_bf16(acc / L, 0.f));
   if (f == 0 && p.lse) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
 }
