@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -29,16 +30,8 @@ class FaError(RuntimeError):
         super().__init__(f"{where}: {lib().fa_status_string(code).decode()} ({code})")
 
 
-class _PagedCache(ctypes.Structure):
-    """``fa_paged_cache`` of include/fa_cache.h."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
-                ("k_stride", ctypes.c_longlong * 3), ("v_stride", ctypes.c_longlong * 3),
-                ("k_scale_stride", ctypes.c_longlong * 3), ("v_scale_stride", ctypes.c_longlong * 3),
-                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
-                ("block_table_stride", ctypes.c_longlong), ("type", ctypes.c_int), ("num_pages", ctypes.c_int),
-                ("H", ctypes.c_int), ("page_size", ctypes.c_int), ("d", ctypes.c_int), ("B", ctypes.c_int),
-                ("max_pages", ctypes.c_int)]
+# ``fa_paged_cache`` of include/fa_cache.h, packed into bytes: pointers, strides, then ints.
+_PAGED_CACHE = struct.Struct("@4P12q2Pq7i4x")
 
 
 _lib = None
@@ -91,8 +84,8 @@ def lib() -> ctypes.CDLL:
         L.fa_noalloc_device_status.restype = i
         L.fa_noalloc_selftest_timeout.argtypes = [vp]
         L.fa_noalloc_selftest_timeout.restype = i
-        pc, pll = ctypes.POINTER(_PagedCache), ctypes.POINTER(ctypes.c_longlong)
-        L.fa_cache_append.argtypes = [pc, vp, vp, pll, pll, i, vp, vp]
+        pc = ctypes.c_char_p  # a fa_paged_cache, packed by _paged_cache
+        L.fa_cache_append.argtypes = [pc, vp, vp, ctypes.c_char_p, ctypes.c_char_p, i, vp, vp]
         L.fa_cache_append.restype = i
         L.fa_cache_gather.argtypes = [pc, vp, vp, i, i, vp]
         L.fa_cache_gather.restype = i
@@ -348,65 +341,72 @@ def fa_dropout_mask(B: int, H: int, N: int, rate: float, seed: int, offset: int,
 
 
 # ------------------------------------------------------------ key/value cache
-_LL2, _LL3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
 CACHE_BF16, CACHE_E4M3 = 0, 1
+_STRIDES2 = struct.Struct("@2q")
+_ZERO6 = (0,) * 6
 
 
-def _check_on(t, name: str, dtype, shape, device):
+def _check_on(t, name: str, dtype, shape, device: int):
     """Type, device and shape of a tensor whose strides the caller deals with."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale) -> _PagedCache:
-    """The C description of a cache held in torch tensors (any strides with adjacent row elements)."""
+def _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale):
+    """The packed C description of a cache held in torch tensors (any strides with adjacent
+    row elements), and (device, B, H, d)."""
     if not isinstance(k_cache, torch.Tensor) or not isinstance(block_table, torch.Tensor):
         raise TypeError("k_cache and block_table must be torch.Tensor")
-    dt, dev = k_cache.dtype, k_cache.device
-    if dt != torch.bfloat16 and dt != torch.uint8:
+    dt, dev = k_cache.dtype, k_cache.get_device()
+    e4m3 = dt == torch.uint8
+    if not e4m3 and dt != torch.bfloat16:
         raise TypeError(f"k_cache must be torch.bfloat16 or torch.uint8 (e4m3 codes), got {dt}")
-    if dev.type != "cuda":
+    if not k_cache.is_cuda:
         raise ValueError("k_cache must be a CUDA tensor")
-    if k_cache.dim() != 4 or block_table.dim() != 2:
+    shape, table = k_cache.shape, block_table.shape
+    if len(shape) != 4 or len(table) != 2:
         raise ValueError("k_cache is [pages, H, page_size, d] and block_table [B, max_pages]")
-    shape = k_cache.shape
     P, H, page, d = shape
-    B, per = block_table.shape
+    B, per = table
     _check_on(v_cache, "v_cache", dt, shape, dev)
-    _check_on(block_table, "block_table", torch.int32, (B, per), dev)
-    _check_on(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _check_on(block_table, "block_table", torch.int32, table, dev)
+    _check_on(seq_lens, "seq_lens", torch.int32, table[:1], dev)
     ks, vs, bs = k_cache.stride(), v_cache.stride(), block_table.stride()
-    if (d > 1 and (ks[3] != 1 or vs[3] != 1)) or (per > 1 and bs[1] != 1) or not seq_lens.is_contiguous():
+    if (d > 1 and (ks[3] != 1 or vs[3] != 1)) or (per > 1 and bs[1] != 1) or (B > 1 and seq_lens.stride(0) != 1):
         raise ValueError("the last dimension of k_cache, v_cache, block_table and seq_lens must be contiguous")
-    if dt == torch.uint8:
+    scales = (None, None)
+    fs = _ZERO6
+    if e4m3:
         _check_on(k_scale, "k_scale", torch.float32, shape[:3], dev)
         _check_on(v_scale, "v_scale", torch.float32, shape[:3], dev)
-        return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                           _LL3(*ks[:3]), _LL3(*vs[:3]), _LL3(*k_scale.stride()), _LL3(*v_scale.stride()),
-                           block_table.data_ptr(), seq_lens.data_ptr(), bs[0], CACHE_E4M3, P, H, page, d, B, per)
-    if k_scale is not None or v_scale is not None:
+        scales = (k_scale.data_ptr(), v_scale.data_ptr())
+        fs = k_scale.stride() + v_scale.stride()
+    elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale belong to a cache of e4m3 codes (torch.uint8)")
-    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), None, None, _LL3(*ks[:3]), _LL3(*vs[:3]), _LL3(),
-                       _LL3(), block_table.data_ptr(), seq_lens.data_ptr(), bs[0], CACHE_BF16, P, H, page, d, B, per)
+    return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), scales[0] or 0, scales[1] or 0, *ks[:3], *vs[:3],
+                             *fs, block_table.data_ptr(), seq_lens.data_ptr(), bs[0], CACHE_E4M3 if e4m3 else CACHE_BF16,
+                             P, H, page, d, B, per), dev, B, H, d
 
 
-def _call_on(device, where: str, stream, fn, *args) -> None:
+def _call_on(device: int, where: str, stream, fn, *args) -> None:
     """Call a C entry point with ``device`` current, on ``stream`` (its current stream by default)."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{device}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, handle)
     if rc != FA_OK:
         raise FaError(rc, where)
 
@@ -422,26 +422,25 @@ def fa_cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_ne
     the lengths after the write.  ``cu_new`` None: one token per sequence (T = B);
     else int32 [B + 1], tokens ``cu_new[b]:cu_new[b+1]`` end sequence b.
     """
-    c = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
-    dev = k_cache.device
+    c, dev, B, H, d = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
         raise ValueError("k_new must be a [T, H, d] tensor")
     T = k_new.shape[0]
-    _check_on(k_new, "k_new", torch.bfloat16, (T, c.H, c.d), dev)
-    _check_on(v_new, "v_new", torch.bfloat16, (T, c.H, c.d), dev)
+    _check_on(k_new, "k_new", torch.bfloat16, (T, H, d), dev)
+    _check_on(v_new, "v_new", torch.bfloat16, (T, H, d), dev)
     ks, vs = k_new.stride(), v_new.stride()
     if T and (ks[2] != 1 or vs[2] != 1):
         raise ValueError("the last dimension of k_new and v_new must be contiguous")
     cu = None
     if cu_new is not None:
-        _check_on(cu_new, "cu_new", torch.int32, (c.B + 1,), dev)
+        _check_on(cu_new, "cu_new", torch.int32, (B + 1,), dev)
         if not cu_new.is_contiguous():
             raise ValueError("cu_new must be contiguous")
         cu = cu_new.data_ptr()
-    elif T != c.B:
-        raise ValueError(f"k_new has {T} tokens for {c.B} sequences: pass cu_new")
-    _call_on(dev, "fa_cache_append", stream, lib().fa_cache_append, c, k_new.data_ptr(), v_new.data_ptr(),
-             _LL2(*ks[:2]), _LL2(*vs[:2]), T, cu)
+    elif T != B:
+        raise ValueError(f"k_new has {T} tokens for {B} sequences: pass cu_new")
+    _call_on(dev, "fa_cache_append", stream, _lib.fa_cache_append, c, k_new.data_ptr(), v_new.data_ptr(),
+             _STRIDES2.pack(ks[0], ks[1]), _STRIDES2.pack(vs[0], vs[1]), T, cu)
 
 
 def fa_cache_gather(k_cache, v_cache, block_table, seq_lens, k_out, v_out, k_scale=None, v_scale=None,
@@ -452,18 +451,18 @@ def fa_cache_gather(k_cache, v_cache, block_table, seq_lens, k_out, v_out, k_sca
     repeated ``rep`` times (from the outputs' shape): the K and V that ``fa_fwd``
     takes.  ``k_out`` or ``v_out`` may be None.  The cache is as in ``fa_cache_append``.
     """
-    c = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
+    c, dev, B, H, d = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
     out = k_out if k_out is not None else v_out
-    if not isinstance(out, torch.Tensor) or out.dim() != 4 or out.shape[1] % c.H != 0:
-        raise ValueError(f"k_out and v_out are [B, {c.H} * rep, N, d] tensors, and one of them is needed")
-    shape = (c.B, out.shape[1], out.shape[2], c.d)
+    if not isinstance(out, torch.Tensor) or out.dim() != 4 or out.shape[1] % H != 0:
+        raise ValueError(f"k_out and v_out are [B, {H} * rep, N, d] tensors, and one of them is needed")
+    shape = (B, out.shape[1], out.shape[2], d)
     for nm, t in (("k_out", k_out), ("v_out", v_out)):
         if t is not None:
-            _check_on(t, nm, torch.bfloat16, shape, k_cache.device)
-            _check(t, nm, torch.bfloat16)
-    _call_on(k_cache.device, "fa_cache_gather", stream, lib().fa_cache_gather, c,
-             None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
-             shape[1] // c.H, shape[2])
+            _check_on(t, nm, torch.bfloat16, shape, dev)
+            if not t.is_contiguous():
+                raise ValueError(f"{nm} must be contiguous")
+    _call_on(dev, "fa_cache_gather", stream, _lib.fa_cache_gather, c, None if k_out is None else k_out.data_ptr(),
+             None if v_out is None else v_out.data_ptr(), shape[1] // H, shape[2])
 
 
 def fa_decode_workspace_bytes(B: int, Hq: int, H: int, d: int) -> int:
@@ -479,25 +478,22 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
     ``window``: how many of a sequence's last positions are seen (0: all).  The cache
     is as in ``fa_cache_append``, the new token's key and value already in it.
     """
-    c = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
-    dev = k_cache.device
+    c, dev, B, _, d = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [B, Hq, d] tensor")
-    shape = (c.B, q.shape[1], c.d)
-    for nm, t in (("q", q), ("o", o)):
-        _check_on(t, nm, torch.bfloat16, shape, dev)
-        if not t.is_contiguous():
-            raise ValueError(f"{nm} must be contiguous")
+    Hq = q.shape[1]
+    _check_on(q, "q", torch.bfloat16, (B, Hq, d), dev)
+    _check_on(o, "o", torch.bfloat16, (B, Hq, d), dev)
     lse_ptr = None
     if lse is not None:
-        _check_on(lse, "lse", torch.float32, shape[:2], dev)
+        _check_on(lse, "lse", torch.float32, (B, Hq), dev)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
         lse_ptr = lse.data_ptr()
     if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace must be a torch.Tensor")
     _check_on(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _call_on(dev, "fa_decode", stream, lib().fa_decode, c, q.data_ptr(), o.data_ptr(), lse_ptr, shape[1],
-             float(scale), int(window), workspace.data_ptr(), workspace.numel())
+    if not (q.is_contiguous() and o.is_contiguous() and workspace.is_contiguous()):
+        raise ValueError("q, o and workspace must be contiguous")
+    _call_on(dev, "fa_decode", stream, _lib.fa_decode, c, q.data_ptr(), o.data_ptr(), lse_ptr, Hq, scale, window,
+             workspace.data_ptr(), workspace.numel())

@@ -3,9 +3,9 @@ library exports what include/fa_cache.h declares, and refuses bad arguments with
 the documented status codes before touching any device."""
 from __future__ import annotations
 
-import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -25,18 +25,30 @@ def fa():
 
 def cache(fa, **kw):
     """A valid description: 10 pages of 64 tokens, 4 heads, d = 128, [pages, H, page, d]."""
-    LL3 = ctypes.c_longlong * 3
     c = dict(k=P, v=P, k_scale=P, v_scale=P, k_stride=(4 * 64 * 128, 64 * 128, 128),
              v_stride=(4 * 64 * 128, 64 * 128, 128), k_scale_stride=(256, 64, 1), v_scale_stride=(256, 64, 1),
              block_table=P, seq_lens=P, block_table_stride=7, type=1, num_pages=10, H=4, page_size=64, d=128, B=3,
              max_pages=7)
     c.update(kw)
-    return fa._PagedCache(**{k: (LL3(*v) if isinstance(v, tuple) else v) for k, v in c.items()})
+    return Packed(fa, c)
+
+
+class Packed(bytes):
+    """fa_paged_cache as bytes, in the header's field order, with the fields at hand."""
+    ORDER = ("k", "v", "k_scale", "v_scale", "k_stride", "v_stride", "k_scale_stride", "v_scale_stride", "block_table",
+             "seq_lens", "block_table_stride", "type", "num_pages", "H", "page_size", "d", "B", "max_pages")
+
+    def __new__(cls, fa, c):
+        vals = []
+        for nm in cls.ORDER:
+            vals += c[nm] if isinstance(c[nm], tuple) else [c[nm] or 0]
+        self = super().__new__(cls, fa._PAGED_CACHE.pack(*vals))
+        self.B, self.H = c["B"], c["H"]
+        return self
 
 
 def append(fa, c, k=P, v=P, ks=(512, 128), vs=(512, 128), T=3, cu=None):
-    LL2 = ctypes.c_longlong * 2
-    return fa.lib().fa_cache_append(c, k, v, LL2(*ks), LL2(*vs), T, cu, None)
+    return fa.lib().fa_cache_append(c, k, v, fa._STRIDES2.pack(*ks), fa._STRIDES2.pack(*vs), T, cu, None)
 
 
 def gather(fa, c, k=P, v=P, rep=2, N=100):
@@ -84,6 +96,22 @@ def test_every_call_refuses_a_bad_cache(fa, kw, code):
     assert append(fa, c, T=T) == code
     assert gather(fa, c) == code
     assert decode(fa, c, Hq=8 * max(c.H, 1)) == code
+
+
+def test_packed_description_is_the_header_s_struct(fa, tmp_path):
+    """Size and field offsets of fa_paged_cache, from a C compiler."""
+    src = tmp_path / "t.c"
+    src.write_text('#include <stdio.h>\n#include "fa_cache.h"\nint main(void) { fa_paged_cache c; (void)c; printf("%zu", sizeof(c));'
+                   + "".join(f' printf(" %zu", offsetof(fa_paged_cache, {nm}));' for nm in Packed.ORDER) + " return 0; }\n")
+    exe = tmp_path / "t"
+    subprocess.check_call(["gcc", "-I", os.path.dirname(HEADER), str(src), "-o", str(exe)])
+    got = [int(x) for x in subprocess.check_output([str(exe)]).split()]
+    want, at = [], 0
+    for nm in Packed.ORDER:
+        want.append(at)
+        at += 24 if nm.endswith("_stride") and nm != "block_table_stride" else 4 if nm in Packed.ORDER[11:] else 8
+    assert got[1:] == want
+    assert got[0] == fa._PAGED_CACHE.size
 
 
 def test_null_cache(fa):
