@@ -141,13 +141,35 @@ __device__ __forceinline__ uint32_t swizzled(int row, int byte) {
   return static_cast<uint32_t>(row * ROW + (byte ^ (f << 4)));
 }
 
-// mbar_wait with its slow path out of line (the waits are many, and instruction fetch is
-// what the roles of a CTA compete for).
-__device__ __noinline__ bool decode_wait_slow(const WaitCtx &c, uint64_t *bar, uint32_t parity, int tag) {
-  return mbar_wait(c, bar, parity, tag);
+// mbar_wait for a CTA of many waiting warps: the test may suspend the warp for some
+// microseconds (without the hint, the roles' polling took most of the issue slots), and
+// what follows a failed one is out of line (instruction fetch is scarce too).
+__device__ __forceinline__ bool decode_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool decode_wait_slow(const WaitCtx &c, uint32_t bar, uint32_t parity, int tag) {
+  const uint64_t t0 = globaltimer();
+  while (!decode_try_wait(bar, parity)) {
+    if (*c.abort || reinterpret_cast<volatile int *>(c.status)[4] == c.seq) {
+      *c.abort = 1;
+      return false;
+    }
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      record_failure(c, kStatusTimeout, tag);
+      return false;
+    }
+  }
+  return true;
 }
 __device__ __forceinline__ bool decode_wait(const WaitCtx &c, uint64_t *bar, uint32_t parity, int tag) {
-  return mbar_try_wait(smem_u32(bar), parity) || decode_wait_slow(c, bar, parity, tag);
+  const uint32_t b = smem_u32(bar);
+  return decode_try_wait(b, parity) || decode_wait_slow(c, b, parity, tag);
 }
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
@@ -891,13 +913,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             const uint32_t top = __float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)));
             // The next power of two, within [2^-120, 2^126].
             const uint32_t up = (min(top, 0x7e800000u) + 0x7fffffu) & 0x7f800000u;
-            float now = __uint_as_float(max(up, 7u << 23));
+            uint32_t now = max(up, 7u << 23);
             if (i > 0) {
-              now = fmaxf(now, vref);
-              vscale = vref / now;
+              const uint32_t old = __float_as_uint(vref);
+              now = max(now, old);
+              // old / now, a power of two (or 0 below the normal ones).
+              vscale = __uint_as_float(static_cast<uint32_t>(max(static_cast<int>((127u << 23) + old - now), 0)));
             }
-            vref = now;
-            vinv = C::kWeight / now;
+            vref = __uint_as_float(now);
+            vinv = __uint_as_float((259u << 23) - now);  // kWeight / now, kWeight = 2^5
           }
           // Column lane / 4's maximum; -1e30 stands in for -inf, so that differences stay defined.
           const float4 m4 = *reinterpret_cast<const float4 *>(xr + (lane & ~3));
@@ -997,7 +1021,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       if (w4 == 0 && lane == 0) {
 #pragma unroll
         for (int g = 0; g < 8; ++g) mstat[ob * GB + 8 * grp + g] = -m[g];
-        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = 1.f / vinv;
+        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = vref * (1.f / C::kWeight);
       }
       __syncwarp();
       if (lane == 0) {
