@@ -28,6 +28,7 @@ struct CacheView {
   const int *seq_lens;
   long long bt_stride;
   int num_pages, H, page_size, B, max_pages;
+  int cap;         // max_pages * page_size: the longest sequence
   int page_shift;  // log2(page_size), or -1: then page_size is a multiple of 128
   unsigned long long page_magic;  // ceil(2^64 / (page_size / 128)), where page_shift is -1
   int *status;
@@ -49,10 +50,9 @@ __device__ __noinline__ void record_cache_error(int *status, int kernel, int b, 
 // Sequence b's length, clamped to what its row of the block table can hold.
 __device__ __forceinline__ int cache_len(const CacheView &c, int b, int kernel) {
   const int n = __ldg(c.seq_lens + b);
-  const long long cap = static_cast<long long>(c.max_pages) * c.page_size;
-  if (n < 0 || n > cap) {
+  if (n < 0 || n > c.cap) {
     record_cache_error(c.status, kernel, b, c.seq);
-    return n < 0 ? 0 : static_cast<int>(cap);
+    return n < 0 ? 0 : c.cap;
   }
   return n;
 }

@@ -71,6 +71,7 @@ int make_view(const fa_paged_cache *c, fa::CacheView *v, DeviceState **ds) {
   v->page_size = c->page_size;
   v->B = c->B;
   v->max_pages = c->max_pages;
+  v->cap = c->max_pages * c->page_size;
   v->page_shift = -1;
   for (int s = 4; s < 31; ++s)
     if (c->page_size == (1 << s)) v->page_shift = s;
@@ -111,7 +112,7 @@ int encode_cache(CUtensorMap *m, const void *ptr, const fa_paged_cache *c, const
 }
 
 // Query heads per block of the decode kernel: the smallest of its instances that holds G.
-int decode_block(int G) { return G <= 8 ? 8 : G <= 16 ? 16 : 32; }
+int decode_block(int G) { return G <= 2 ? 2 : G <= 4 ? 4 : G <= 8 ? 8 : G <= 16 ? 16 : 32; }
 
 // Workspace: meta, then (m, l) and O of two parts per CTA.
 size_t decode_ml_offset() { return fa::kDecodeMaxCtas * sizeof(int4); }
@@ -153,7 +154,9 @@ cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa
 template <int D, bool E4M3>
 cudaError_t launch_decode_block(int gb, const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p,
                                 int num_sms, long long most, cudaStream_t s) {
-  return gb == 8    ? launch_decode<D, E4M3, 8>(tk, tv, p, num_sms, most, s)
+  return gb == 2    ? launch_decode<D, E4M3, 2>(tk, tv, p, num_sms, most, s)
+         : gb == 4  ? launch_decode<D, E4M3, 4>(tk, tv, p, num_sms, most, s)
+         : gb == 8  ? launch_decode<D, E4M3, 8>(tk, tv, p, num_sms, most, s)
          : gb == 16 ? launch_decode<D, E4M3, 16>(tk, tv, p, num_sms, most, s)
                     : launch_decode<D, E4M3, 32>(tk, tv, p, num_sms, most, s);
 }
@@ -254,11 +257,11 @@ int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, i
   if (!workspace || workspace_bytes < fa_decode_workspace_bytes(cache->B, Hq, cache->H, cache->d))
     return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_MISALIGNED;
-  // The kernel counts tiles of 128 positions, over all sequences and heads, in 31 bits.
+  // The kernel counts the cost of tiles of 128 positions, over all sequences and heads, in 31 bits.
   const int G = Hq / cache->H, gb = decode_block(G), nblk = (G + gb - 1) / gb;
   const long long item_tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 127) / 128;
   const long double most = static_cast<long double>(cache->B) * cache->H * nblk * item_tiles;
-  if (most >= 2147483648.0L) return FA_ERR_UNSUPPORTED;
+  if (most * 8 >= 2147483648.0L) return FA_ERR_UNSUPPORTED;  // kItemCost + kTileCost = 8
   fa::DecodeParams p;
   DeviceState *ds = nullptr;
   st = make_view(cache, &p.c, &ds);

@@ -53,7 +53,7 @@ struct DecodeParams {
   int window;         // 0: all positions
   int vec_scales;     // e4m3: four neighbouring tokens' factors are one aligned 16-byte piece
   float scale_log2;   // scale * log2(e)
-  int4 *meta;         // [kDecodeMaxCtas] item whose parts start at CTA c: {b, first query head, parts, -}; parts 0: none
+  int4 *meta;         // [kDecodeMaxCtas] the item whose parts start at CTA c: {b, first query head, parts, -}; parts 0: none
   float2 *part_ml;    // [2 * kDecodeMaxCtas][GB] (m, l) of a part
   float *part_o;      // [2 * kDecodeMaxCtas][GB][d]
 };
@@ -66,12 +66,14 @@ struct DecodeCfg {
   static constexpr int kPanels = kRowBytes / kPanelRow;
   static constexpr int kPanelBytes = 128 * kPanelRow;
   static constexpr int kTileBytes = 128 * kRowBytes;
-  static constexpr int kGroups = GB / 8;                           // softmax warp groups
-  static constexpr int kQRows = E4M3 ? 2 * GB : GB;                // rows of Q in shared memory
+  static constexpr int kHeads = GB < 8 ? GB : 8;                   // query heads per softmax thread
+  static constexpr int kGroups = GB / kHeads;                      // softmax warp groups
+  static constexpr int kQUsed = E4M3 ? 2 * GB : GB;                // rows of Q that are written
+  static constexpr int kQRows = kQUsed < 8 ? 8 : kQUsed;           // rows of Q in shared memory
   static constexpr int kQCols = kQRows < 16 ? 16 : kQRows;         // columns of S^T
   static constexpr int kOParts = E4M3 ? 3 : 2;
   static constexpr int kOCols = (kOParts * GB + 15) / 16 * 16;     // columns of O^T
-  static constexpr int kPRow = E4M3 ? (GB == 8 ? 32 : GB == 16 ? 64 : 128) : 4 * GB;  // bytes of a key's row of P
+  static constexpr int kPRow = GB <= 8 ? 32 : 4 * GB;              // bytes of a key's row of P
   static constexpr int kQBytes = kQRows * kRowBytes;
   static constexpr int kPBytes = 128 * kPRow;
   static constexpr int kScStages = 4;  // ring of the keys' factors (e4m3)
@@ -83,8 +85,11 @@ struct DecodeCfg {
   static constexpr int kSoftmaxWarps = 4 * kGroups;
   static constexpr int kWarps = kSoftmaxWarps + 8;  // softmax, 4 epilogue, producer, issuer, Q, scales
   static constexpr int kThreads = 32 * kWarps;
-  // Two CTAs per SM with 8 heads: one's tile hides the other's waits.
-  static constexpr int kCtas = GB == 8 ? 2 : 1;
+  // Two CTAs per SM with up to 8 heads: one's tile hides the other's waits.
+  static constexpr int kCtas = GB <= 8 ? 2 : 1;
+  // The share of a CTA is dealt out by cost: kTileCost a tile, and kItemCost for what an item
+  // costs besides (its Q, first maximum, sums and epilogue).
+  static constexpr int kTileCost = 4, kItemCost = 4;
   static constexpr int kSmemMax = kCtas == 2 ? 115712 : 232448;
 
   static constexpr int kPOff = 0;
@@ -95,7 +100,7 @@ struct DecodeCfg {
   static constexpr int kScBytes = E4M3 ? kScStages * 1024 : 0;
   static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + 2 * kGroups + 8 * kGroups + 2 * kGroups;
   static constexpr int kFixedBars = 20 + 2 * kScStages;
-  static constexpr int kTailBytes = kScBytes + kMiscFloats * 4 + kFixedBars * 8 + 12 * 4;
+  static constexpr int kTailBytes = kScBytes + kMiscFloats * 4 + kFixedBars * 8 + 16 * 4;
   static constexpr int kFit = (kSmemMax - kRingOff - kTailBytes) / (kTileBytes + 16);
   static constexpr int kSlots = kFit > 24 ? 24 : kFit;
   static constexpr int kScOff = kRingOff + kSlots * kTileBytes;
@@ -172,16 +177,37 @@ __device__ __forceinline__ bool decode_wait(const WaitCtx &c, uint64_t *bar, uin
   return decode_try_wait(b, parity) || decode_wait_slow(c, b, parity, tag);
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
+// N = 2, 4 or 8 columns of this thread's tensor memory lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t *r) {
+  if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  else if constexpr (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t *r) {
+  if constexpr (N == 8)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  else if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
@@ -258,14 +284,17 @@ __device__ __forceinline__ void reduce_columns(float (&v)[N], F f) {
   for (; bit >= 1; bit >>= 1) v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
 }
 
-// `total` tiles dealt out to `nc` CTAs, the first of them one more where it does not divide.
+// `total` units of cost dealt out to `nc` CTAs, the first of them one more where it does not
+// divide.  A unit x of an item that begins at x0 stands for its tile (x - x0 - kItemCost) /
+// kTileCost (the first one below), so a CTA's tiles are those between the tiles that its
+// first unit and the next CTA's stand for.
 struct DecodeSplit {
   int q, r;
   __device__ __forceinline__ DecodeSplit(int total, int nc) : q(total / nc), r(total % nc) {}
   __device__ __forceinline__ int begin(int c) const { return q * c + min(c, r); }
-  __device__ __forceinline__ int owner(int tile) const {
+  __device__ __forceinline__ int owner(int x) const {
     const int wide = r * (q + 1);
-    return tile < wide ? tile / (q + 1) : r + (tile - wide) / q;
+    return x < wide ? x / (q + 1) : r + (x - wide) / q;
   }
 };
 
@@ -274,19 +303,20 @@ struct DecodeSplit {
 struct DecodeNext {
   int b, base, lane_len;
 };
-__device__ __noinline__ DecodeNext decode_next(const DecodeParams &p, int b, int base, int lane_len) {
+__device__ __noinline__ DecodeNext decode_next(const int *seq_lens, int B, int b, int base, int lane_len) {
   for (;;) {
     const uint32_t later = __ballot_sync(0xffffffffu, lane_len > 0 && base + static_cast<int>(lane_id()) > b);
     if (later) return {base + __ffs(later) - 1, base, lane_len};
     base += 32;
-    if (base >= p.c.B) return {-1, base, 0};
+    if (base >= B) return {-1, base, 0};
     const int i = base + static_cast<int>(lane_id());
-    lane_len = i < p.c.B ? cache_len(p.c, i, kKernelDecode) : 0;
+    lane_len = i < B ? __ldg(seq_lens + i) : 0;
   }
 }
 
 // A walk over this CTA's tiles, run by a whole warp.  Lane i holds the length of sequence
-// base + i, so that moving on to another sequence costs a load once in 32.
+// base + i as it is in memory, so that moving on to another sequence costs a load once in 32
+// (and the first one none: the share brings its length).
 struct DecodeWalk {
   int b, h, blk, off, rem;   // sequence, cache head, block of query heads, tile of the item, tiles left to this CTA
   int len, first, tile0, n;  // b's length, first visible position, its tile, and the item's tiles
@@ -295,25 +325,21 @@ struct DecodeWalk {
   __device__ __forceinline__ static int first_of(const DecodeParams &p, int len) {
     return p.window > 0 ? max(0, len - p.window) : 0;
   }
-  __device__ __forceinline__ void sequence(const DecodeParams &p) {
-    len = __shfl_sync(0xffffffffu, lane_len, b - base);
+  __device__ __forceinline__ void sequence(const DecodeParams &p, int raw) {
+    len = min(raw, p.c.cap);
     first = first_of(p, len);
     tile0 = first >> 7;
     n = ((len + 127) >> 7) - tile0;
   }
   __device__ __forceinline__ void start(const DecodeParams &p, const int *share) {
+    base = b = share[0];
     h = share[1];
-    blk = share[6];
     off = share[2];
-    rem = share[3];
-    b = base = lane_len = len = first = tile0 = n = 0;
-    if (rem > 0) {
-      const DecodeNext nx = decode_next(p, share[0] - 1, share[0] - 32, 0);
-      b = nx.b;
-      base = nx.base;
-      lane_len = nx.lane_len;
-      sequence(p);
-    }
+    rem = share[7] ? 0 : share[11] - share[10];
+    blk = share[6];
+    const int i = b + static_cast<int>(lane_id());
+    lane_len = rem > 0 && i < p.c.B ? __ldg(p.c.seq_lens + i) : 0;
+    sequence(p, share[8]);
   }
   // Tiles of the current segment: the item's tiles from `off` on, as far as the share goes.
   __device__ __forceinline__ int run() const { return min(n - off, rem); }
@@ -327,7 +353,7 @@ struct DecodeWalk {
     blk = 0;
     if (++h < p.c.H) return;
     h = 0;
-    const DecodeNext nx = decode_next(p, b, base, lane_len);
+    const DecodeNext nx = decode_next(p.c.seq_lens, p.c.B, b, base, lane_len);
     if (nx.b < 0) {  // not reached while tiles are left
       rem = 0;
       return;
@@ -335,7 +361,7 @@ struct DecodeWalk {
     b = nx.b;
     base = nx.base;
     lane_len = nx.lane_len;
-    sequence(p);
+    sequence(p, __shfl_sync(0xffffffffu, lane_len, b - base));
   }
 };
 
@@ -376,7 +402,7 @@ struct DecodePages {
           __ballot_sync(0xffffffffu, wk.lane_len > 0 && wk.base + static_cast<int>(lane_id()) > b);
       if (later) {
         nb = wk.base + __ffs(later) - 1;
-        const int len = __shfl_sync(0xffffffffu, wk.lane_len, nb - wk.base);
+        const int len = min(__shfl_sync(0xffffffffu, wk.lane_len, nb - wk.base), c.cap);
         const int first = DecodeWalk::first_of(p, len);
         nblk = cache_page_index(c, first & ~127) >> 5;
         nids = load(c, nb, nblk, len, first);
@@ -412,8 +438,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   int *words = reinterpret_cast<int *>(bars + C::kFixedBars);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(words);
   volatile int *abort_flag = words + 1;
-  int *share = words + 2;  // first sequence, head, tile and the number of tiles, T, nc, block of heads, "do nothing"
-  uint64_t *bar_full = reinterpret_cast<uint64_t *>(words + 12);  // [kSlots]
+  // The share: first sequence, head and tile, -; total cost, CTAs with a share, first block of
+  // heads, "do nothing"; first sequence's length, cost before the first item, first and end tile.
+  int *share = words + 2;
+  uint64_t *bar_full = reinterpret_cast<uint64_t *>(words + 16);  // [kSlots]
   uint64_t *bar_empty = bar_full + C::kSlots;                     // [kSlots]
   float *xmax = reinterpret_cast<float *>(smem + C::kMiscOff);    // [2][GB][4]
   float *lpart = xmax + 2 * GB * 4;                               // [2][4][GB]
@@ -427,10 +455,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const WaitCtx ctx{p.c.status, abort_flag, kKernelDecode, p.c.seq};
+  // This thread's first sequence for the share below; the load runs while barriers are set up.
+  const int per = (p.c.B + C::kThreads - 1) / C::kThreads;
+  const int b_lo = min(p.c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.c.B, b_lo + per);
+  const int len_lo = b_lo < b_hi ? __ldg(p.c.seq_lens + b_lo) : 0;
   // The join kernel may be put on the SMs' leftovers now; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == 0) {
+  if (warp == C::kQWarp) {
     if (lane < 2) {
       mbar_init(&bar_q[lane], 32);
       // The issuer's commit; e4m3: and the softmax warps, for q's scale.
@@ -451,7 +483,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       mbar_init(&bar_full[lane], 1);
       mbar_init(&bar_empty[lane], 1);
     }
-    if (lane < 8) share[lane] = 0;
+    if (lane < 12) share[lane] = 0;
     __syncwarp();
     if (lane == 0) {
       mbar_init(bar_drain, 1);
@@ -472,56 +504,75 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   }
 
   // ---------------------------------------------------------------- the share
-  // Thread i counts the tiles of sequences [i * per, (i + 1) * per); a scan over the
+  // Thread i counts tiles and cost of sequences [i * per, (i + 1) * per); a scan over the
   // threads gives every share's first sequence.
   {
     const int items = p.c.H * p.nblk;
-    const int per = (p.c.B + C::kThreads - 1) / C::kThreads;
-    const int b_lo = min(p.c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.c.B, b_lo + per);
     auto tiles_of = [&](int b) {
-      const int len = cache_len(p.c, b, kKernelDecode);
-      const int first = p.window > 0 ? max(0, len - p.window) : 0;
-      return ((len + 127) >> 7) - (first >> 7);
+      const int raw = b == b_lo ? len_lo : __ldg(p.c.seq_lens + b);
+      const int len = min(max(raw, 0), p.c.cap);
+      if (raw != len) record_cache_error(p.c.status, kKernelDecode, b, p.c.seq);
+      return ((len + 127) >> 7) - (DecodeWalk::first_of(p, len) >> 7);
     };
-    int mine = 0;
+    auto cost_of = [&](int n) { return n > 0 ? (C::kItemCost + C::kTileCost * n) * items : 0; };
+    int tiles = 0, cost = 0;
 #pragma unroll 1
-    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(b) * items;
-    int incl = mine;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const int n = tiles_of(b);
+      tiles += n * items;
+      cost += cost_of(n);
+    }
+    int it = tiles, ic = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+      const int ut = __shfl_up_sync(0xffffffffu, it, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
+      if (lane >= o) {
+        it += ut;
+        ic += uc;
+      }
     }
-    int *sums = reinterpret_cast<int *>(xmax);  // [kWarps], used before the softmax warps start
-    static_assert(C::kWarps <= 2 * GB * 4, "the scan's sums fit");
-    if (lane == 31) sums[warp] = incl;
+    int2 *sums = reinterpret_cast<int2 *>(smem);  // [kWarps], before anything else is there
+    if (lane == 31) sums[warp] = make_int2(it, ic);
     __syncthreads();
-    int before = 0, total = 0;
+    int total_t = 0, total_c = 0, before_t = it - tiles, before_c = ic - cost;
+#pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+      const int2 v = sums[w];
+      if (w < warp) {
+        before_t += v.x;
+        before_c += v.y;
+      }
+      total_t += v.x;
+      total_c += v.y;
     }
-    const int nc = min(static_cast<int>(gridDim.x), total), c = static_cast<int>(blockIdx.x);
+    const int nc = min(static_cast<int>(gridDim.x), total_t), c = static_cast<int>(blockIdx.x);
     if (c < nc) {
-      const DecodeSplit sp(total, nc);
-      const int t0 = sp.begin(c);
-      const int excl = before + incl - mine;
-      if (mine > 0 && t0 >= excl && t0 < excl + mine) {
-        int b = b_lo, at = t0 - excl;
-        int n = tiles_of(b);
+      const DecodeSplit sp(total_c, nc);
 #pragma unroll 1
-        while (at >= n * items) {
-          at -= n * items;
+      for (int e = 0; e < 2; ++e) {  // the share's first unit, and the next share's
+        const int x = sp.begin(c + e);
+        if (e == 1 && x == total_c && threadIdx.x == 0) share[11] = total_t;
+        if (cost == 0 || x < before_c || x >= before_c + cost) continue;
+        int b = b_lo, n = tiles_of(b), at = x - before_c, t0 = before_t;
+#pragma unroll 1
+        while (at >= cost_of(n)) {
+          at -= cost_of(n);
+          t0 += n * items;
           n = tiles_of(++b);
         }
-        share[0] = b;
-        const int item = at / n;
-        share[1] = item / p.nblk;
-        share[2] = at % n;
-        share[3] = share[7] ? 0 : sp.begin(c + 1) - t0;
-        share[4] = total;
-        share[5] = nc;
-        share[6] = item % p.nblk;
+        const int one = C::kItemCost + C::kTileCost * n, item = at / one;
+        const int off = max(at - item * one - C::kItemCost, 0) / C::kTileCost;
+        share[10 + e] = t0 + item * n + off;
+        if (e == 0) {
+          share[0] = b;
+          share[1] = p.nblk == 1 ? item : item / p.nblk;
+          share[2] = off;
+          share[6] = p.nblk == 1 ? 0 : item % p.nblk;
+          share[8] = min(b == b_lo ? len_lo : __ldg(p.c.seq_lens + b), p.c.cap);
+          share[9] = x - at + item * one;
+          share[4] = total_c;
+          share[5] = nc;
+        }
       }
     }
   }
@@ -670,19 +721,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     __syncwarp();
   } else if (warp == C::kQWarp) {
     // ---------------------------------------------------------------- Q rows
-    // Rows of the segment's query heads into swizzled shared memory, 8 at a time; the next
-    // 8 (of this segment or the next) are read meanwhile.  Lane's piece i is 16 bytes, the
-    // (32 i + lane)th of the 8 rows.  Rows past the last head are 0.
-    constexpr int kPieces = D / 32, kPerRow = D / 8;
+    // Rows of the segment's query heads into swizzled shared memory, kHeads at a time; the next
+    // ones (of this segment or the next) are read meanwhile.  Lane's piece i is 16 bytes, the
+    // (32 i + lane)th of the rows.  Rows past the last head are 0.
+    constexpr int kPerRow = D / 8, kAll = C::kHeads * kPerRow, kPieces = (kAll + 31) / 32;
     uint4 w[kPieces];
     auto load = [&](int c) {
-      const int g0 = wk.blk * GB + 8 * c;
+      const int g0 = wk.blk * GB + C::kHeads * c;
       const uint16_t *src = p.q + (static_cast<long long>(wk.b) * p.Hq + wk.h * p.G + g0) * D;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int at = 32 * i + lane;
         w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (wk.rem > 0 && g0 + at / kPerRow < p.G) w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + at);
+        if (wk.rem > 0 && at < kAll && g0 + at / kPerRow < p.G) w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + at);
       }
     };
     bool ok = true;
@@ -702,12 +753,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         if constexpr (!E4M3) {
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
-            const int row = 8 * c + (32 * i + lane) / kPerRow, in = (32 * i + lane) % kPerRow;
+            const int row = C::kHeads * c + (32 * i + lane) / kPerRow, in = (32 * i + lane) % kPerRow;
+            if (kAll % 32 != 0 && 32 * i + lane >= kAll) break;
             st_shared_v4(dst + (in >> 3) * (C::kQRows * 128) + swizzled<128>(row, (in & 7) * 16), v[i].x, v[i].y, v[i].z,
                          v[i].w);
           }
         } else {
-          // Scale the 8 rows by the power of two that brings their largest element into
+          // Scale the rows by the power of two that brings their largest element into
           // [128, 256), then split: hi = e4m3(x), lo = e4m3(16 (x - hi)) (bf16 values are
           // fp16 values in that range).  A row's scores are off by at most 2^-20 of the
           // group's largest.
@@ -738,13 +790,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
               part[0][k >> 1] |= static_cast<uint32_t>(hi) << (16 * (k & 1));
               part[1][k >> 1] |= static_cast<uint32_t>(lo) << (16 * (k & 1));
             }
-            const int row = 8 * c + (32 * i + lane) / kPerRow, byte = (32 * i + lane) % kPerRow * 8;
+            const int row = C::kHeads * c + (32 * i + lane) / kPerRow, byte = (32 * i + lane) % kPerRow * 8;
+            if (kAll % 32 != 0 && 32 * i + lane >= kAll) break;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
-                               dst + swizzled<C::kPanelRow>(k * GB + row, byte & ~15) + (byte & 8)),
-                           "r"(part[k][0]), "r"(part[k][1])
-                           : "memory");
+              st_shared_v2(dst + swizzled<C::kPanelRow>(k * GB + row, byte & ~15) + (byte & 8), part[k][0], part[k][1]);
           }
         }
       }
@@ -795,14 +845,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     }
   } else if (warp < C::kSoftmaxWarps) {
     // -------------------------------------------------------------- softmax
-    // Thread = key (row of S^T, tensor memory lane) and group of 8 heads, kept in pairs.
+    // Thread = key (row of S^T, tensor memory lane) and group of kHeads heads, kept in pairs.
     // All waits are bounded and every thread of the group reaches every bar_any, so a
     // failed wait (`bad`) ends the group's four warps together.
     const int grp = warp >> 2, w4 = warp & 3, key = w4 * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t bar_a = 1 + 2 * grp, bar_b = 2 + 2 * grp;
-    float *xm = xmax + 8 * grp * 4;
-    uint64_t nm2[4], l2[4];           // minus the reference, and this key's sum of weights
+    constexpr int kH = C::kHeads, kPairs = kH / 2, kSpan = 32 / kH;  // kSpan lanes end up with one head's maximum
+    float *xm = xmax + kH * grp * 4;
+    uint64_t nm2[kPairs], l2[kPairs];           // minus the reference, and this key's sum of weights
     float vref = 1.f, vinv = 1.f;     // e4m3: power of two that V's factors are taken relative to; kWeight / vref
     bool bad = false, stop = false;
     int n = 0, nred = 0, sv = 1;      // tiles, reductions, ring slot of the tile's V
@@ -815,7 +866,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         qs = qscale[qb * C::kGroups + grp];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) nm2[i] = l2[i] = 0ull;
+      for (int i = 0; i < kPairs; ++i) nm2[i] = l2[i] = 0ull;
 #pragma unroll 1
       for (int i = 0; i < run; ++i, ++n) {
         const int buf = n & 1;
@@ -832,12 +883,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         }
         __syncwarp();
         tc_fence_after();
-        uint64_t v2[4];  // scores before their factor
+        uint64_t v2[kPairs];  // scores before their factor
         {
-          const uint32_t ts = tmem + lane_off + buf * C::kQCols + 8 * grp;
-          uint32_t hi[8], lo[8];
-          tmem_ld8(ts, hi);
-          if constexpr (E4M3) tmem_ld8(ts + GB, lo);
+          const uint32_t ts = tmem + lane_off + buf * C::kQCols + kH * grp;
+          uint32_t hi[kH], lo[kH];
+          tmem_ld_n<kH>(ts, hi);
+          if constexpr (E4M3) tmem_ld_n<kH>(ts + GB, lo);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
@@ -846,7 +897,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             if constexpr (E4M3) mbar_arrive(&bar_sc_empty[n % C::kScStages]);
           }
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < kPairs; ++g) {
             v2[g] = f2pack(__uint_as_float(hi[2 * g]), __uint_as_float(hi[2 * g + 1]));
             if constexpr (E4M3)
               v2[g] = ffma2(f2pack(__uint_as_float(lo[2 * g]), __uint_as_float(lo[2 * g + 1])), f2pack(0.0625f, 0.0625f),
@@ -860,7 +911,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             f = 1.f;
             fv = 0.f;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) v2[g] = f2pack(-INFINITY, -INFINITY);
+            for (int g = 0; g < kPairs; ++g) v2[g] = f2pack(-INFINITY, -INFINITY);
           }
           // Masked rows of V: weight 0 times whatever the page holds has to be 0.
           if (grp == 0) {
@@ -879,12 +930,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           __syncwarp();
         }
         const uint64_t f2 = f2pack(f, f);
-        float x[8];  // log2 of the weights
+        float x[kH];  // log2 of the weights
         bool grow = true;
         if (i > 0) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
-          const float top = fmaxf(fmax3(fmax3(x[0], x[1], x[2]), x[3], x[4]), fmax3(x[5], x[6], x[7]));
+          for (int g = 0; g < kPairs; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
+          float top = x[0];
+#pragma unroll
+          for (int g = 1; g < kH; ++g) top = fmaxf(top, x[g]);
           grow = top > C::kGrow;
           if constexpr (E4M3) grow |= fabsf(fv) > vref;
           grow = bar_any(bar_a, 128, grow || bad);
@@ -894,11 +947,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           float *xr = xm + (nred & 1) * GB * 4;
           float *vr = vmaxw + grp * 8 + (nred & 1) * 4;
           ++nred;
-          float v[8];
+          float v[kH];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) f2unpack(fmul2(v2[g], f2), v[2 * g], v[2 * g + 1]);
-          reduce_columns<8>(v, [](float a, float b) { return fmaxf(a, b); });
-          if ((lane & 3) == 0) xr[lane + w4] = v[0];
+          for (int g = 0; g < kPairs; ++g) f2unpack(fmul2(v2[g], f2), v[2 * g], v[2 * g + 1]);
+          reduce_columns<kH>(v, [](float a, float b) { return fmaxf(a, b); });
+          if (lane % kSpan == 0) xr[lane / kSpan * 4 + w4] = v[0];
           if constexpr (E4M3) {
             const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
             if (lane == 0) vr[w4] = __uint_as_float(vm);
@@ -923,15 +976,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             vref = __uint_as_float(now);
             vinv = __uint_as_float((259u << 23) - now);  // kWeight / now, kWeight = 2^5
           }
-          // Column lane / 4's maximum; -1e30 stands in for -inf, so that differences stay defined.
-          const float4 m4 = *reinterpret_cast<const float4 *>(xr + (lane & ~3));
+          // Head lane / kSpan's maximum; -1e30 stands in for -inf, so that differences stay defined.
+          const float4 m4 = *reinterpret_cast<const float4 *>(xr + lane / kSpan * 4);
           const float mc = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -1e30f);
-          float alpha[8];
+          float alpha[kH];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < kPairs; ++g) {
             float a, b;
             f2unpack(nm2[g], a, b);
-            float m0 = __shfl_sync(0xffffffffu, mc, 8 * g), m1 = __shfl_sync(0xffffffffu, mc, 8 * g + 4);
+            float m0 = __shfl_sync(0xffffffffu, mc, 2 * g * kSpan), m1 = __shfl_sync(0xffffffffu, mc, (2 * g + 1) * kSpan);
             if (i > 0) {
               m0 = fmaxf(m0, -a);
               m1 = fmaxf(m1, -b);
@@ -946,27 +999,27 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             bad |= !decode_wait(ctx, &bar_p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kTagDPEmpty);
             __syncwarp();
             tc_fence_after();
-            const uint32_t to = tmem + lane_off + kOCol0 + (seg & 1) * C::kOCols + 8 * grp;
+            const uint32_t to = tmem + lane_off + kOCol0 + (seg & 1) * C::kOCols + kH * grp;
 #pragma unroll 1
             for (int part = 0; part < C::kOParts; ++part) {
-              uint32_t o[8];
-              tmem_ld8(to + part * GB, o);
+              uint32_t o[kH];
+              tmem_ld_n<kH>(to + part * GB, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha[e] * vscale));
-              tmem_st8(to + part * GB, o);
+              for (int e = 0; e < kH; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha[e] * vscale));
+              tmem_st_n<kH>(to + part * GB, o);
             }
             tmem_wait_st();
             tc_fence_before();
           }
 #pragma unroll
-          for (int g = 0; g < 4; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
+          for (int g = 0; g < kPairs; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
         }
-        // Weights into P: row = key, this group's 8 heads of each part.
+        // Weights into P: row = key, this group's heads of each part.
         const uint32_t pb = smem_u32(smem + C::kPOff) + buf * C::kPBytes;
-        uint32_t part[C::kOParts][4];
+        uint32_t part[C::kOParts][kPairs];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < kPairs; ++g) {
           const float a = ex2(x[2 * g]), b = ex2(x[2 * g + 1]);
           l2[g] = fadd2(l2[g], f2pack(a, b));
           if constexpr (!E4M3) {
@@ -983,19 +1036,36 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             }
           }
         }
-        if constexpr (!E4M3) {
+        if constexpr (E4M3) {  // two codes a word so far: four
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            st_shared_v4(pb + swizzled<C::kPRow>(key, 2 * (k * GB + 8 * grp)), part[k][0], part[k][1], part[k][2], part[k][3]);
-        } else {
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int g = 0; g < kPairs / 2; ++g) part[k][g] = part[k][2 * g] | (part[k][2 * g + 1] << 16);
+        }
+        constexpr int kPartBytes = kH * C::kElem;  // of this thread, per part
+        if constexpr (kPartBytes == 16) {
+#pragma unroll
+          for (int k = 0; k < C::kOParts; ++k)
+            st_shared_v4(pb + swizzled<C::kPRow>(key, 2 * (k * GB + kH * grp)), part[k][0], part[k][1], part[k][2],
+                         part[k][3]);
+        } else if constexpr (kPartBytes == 8 && E4M3) {
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
-            const int byte = k * GB + 8 * grp;
-            const uint32_t at = pb + swizzled<C::kPRow>(key, byte & ~15) + (byte & 8);
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(part[k][0] | (part[k][1] << 16)),
-                         "r"(part[k][2] | (part[k][3] << 16))
-                         : "memory");
+            const int byte = k * GB + kH * grp;
+            st_shared_v2(pb + swizzled<C::kPRow>(key, byte & ~15) + (byte & 8), part[k][0], part[k][1]);
           }
+        } else if constexpr (!E4M3) {  // 2 or 4 heads: the parts are neighbours
+          const uint32_t at = pb + swizzled<C::kPRow>(key, 0);
+          if constexpr (kH == 4)
+            st_shared_v4(at, part[0][0], part[0][1], part[1][0], part[1][1]);
+          else
+            st_shared_v2(at, part[0][0], part[1][0]);
+        } else {
+          const uint32_t at = pb + swizzled<C::kPRow>(key, 0);
+          if constexpr (kH == 4)
+            st_shared_v4(at, part[0][0], part[1][0], part[2][0], 0u);
+          else
+            st_shared_v2(at, part[0][0] | (part[1][0] << 16), part[2][0]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1010,17 +1080,17 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       const int ob = seg & 1;
       if (seg >= 2) bad |= !decode_wait(ctx, &bar_o_empty[ob], ((seg >> 1) - 1) & 1, kTagDOEmpty);
       __syncwarp();
-      float l[8], m[8];
+      float l[kH], m[kH];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < kPairs; ++g) {
         f2unpack(l2[g], l[2 * g], l[2 * g + 1]);
         f2unpack(nm2[g], m[2 * g], m[2 * g + 1]);
       }
-      reduce_columns<8>(l, [](float a, float b) { return a + b; });
-      if ((lane & 3) == 0) lpart[(ob * 4 + w4) * GB + 8 * grp + (lane >> 2)] = l[0];
+      reduce_columns<kH>(l, [](float a, float b) { return a + b; });
+      if (lane % kSpan == 0) lpart[(ob * 4 + w4) * GB + kH * grp + lane / kSpan] = l[0];
       if (w4 == 0 && lane == 0) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) mstat[ob * GB + 8 * grp + g] = -m[g];
+        for (int g = 0; g < kH; ++g) mstat[ob * GB + kH * grp + g] = -m[g];
         if constexpr (E4M3) vstat[ob * C::kGroups + grp] = vref * (1.f / C::kWeight);
       }
       __syncwarp();
@@ -1048,7 +1118,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     }
     // The item that starts in this CTA's last segment and goes on in the next CTA, if any.
     int4 mt = make_int4(0, 0, 0, 0);
-    const int total = share[4], nc = share[5];
+    const int total = share[4], nc = share[5], c = static_cast<int>(blockIdx.x);
+    int x0 = share[9];  // cost before the walk's item
     bool ok = true;
     for (int seg = 0; wk.rem > 0 && ok; ++seg) {
       const int ob = seg & 1, run = wk.run();
@@ -1060,37 +1131,38 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       tc_fence_after();
       const uint32_t to = tmem + lane_off + kOCol0 + ob * C::kOCols;
       const long long row0 = static_cast<long long>(wk.b) * p.Hq + wk.h * p.G + g0;
-      const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
+      const int slot = 2 * c + (starts ? 1 : 0);
       const bool whole = starts && ends;
+      constexpr int kH = C::kHeads;
 #pragma unroll 1
-      for (int gc = 0; gc < ng; gc += 8) {
-        uint32_t o[C::kOParts][8];
+      for (int gc = 0; gc < (f < D || D == 128 ? ng : 0); gc += kH) {  // d = 64: lanes from 64 on hold nothing new
+        uint32_t o[C::kOParts][kH];
 #pragma unroll
-        for (int part = 0; part < C::kOParts; ++part) tmem_ld8(to + part * GB + gc, o[part]);
-        // Lane g < 8 has head gc + g's sums.
-        const float *lp = lpart + ob * 4 * GB + gc + (lane & 7);
+        for (int part = 0; part < C::kOParts; ++part) tmem_ld_n<kH>(to + part * GB + gc, o[part]);
+        // Lane g < kH has head gc + g's sums.
+        const float *lp = lpart + ob * 4 * GB + gc + (lane & (kH - 1));
         const float lt = (lp[0] + lp[GB]) + (lp[2 * GB] + lp[3 * GB]);
-        const float m8 = mstat[ob * GB + gc + (lane & 7)];
-        float mul = E4M3 ? vstat[ob * C::kGroups + gc / 8] : 1.f;
+        const float mh = mstat[ob * GB + gc + (lane & (kH - 1))];
+        float mul = E4M3 ? vstat[ob * C::kGroups + gc / kH] : 1.f;
         if (whole) mul = __fdividef(mul, lt);
-        if ((warp & 3) == 0 && lane < 8 && gc + lane < ng) {
+        if ((warp & 3) == 0 && lane < kH && gc + lane < ng) {
           if (!whole)
-            p.part_ml[slot * GB + gc + lane] = make_float2(m8, lt);
+            p.part_ml[slot * GB + gc + lane] = make_float2(mh, lt);
           else if (p.lse)
-            p.lse[row0 + gc + lane] = (m8 + log2f(lt)) * 0.69314718055994531f;
+            p.lse[row0 + gc + lane] = (mh + log2f(lt)) * 0.69314718055994531f;
         }
         tmem_wait_ld();
         uint16_t *po = p.o + (row0 + gc) * D + f;
         float *pp = p.part_o + (static_cast<long long>(slot) * GB + gc) * D + f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kH; ++e) {
           float v = __uint_as_float(o[0][e]);
           if constexpr (E4M3)
             v += (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.0625f) * 0.0625f;
           else
             v += __uint_as_float(o[1][e]);
           v *= __shfl_sync(0xffffffffu, mul, e);
-          if (f < D && gc + e < ng) {
+          if (gc + e < ng) {
             if (whole)
               po[e * D] = static_cast<uint16_t>(pack_bf16(v, 0.f));
             else
@@ -1101,13 +1173,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_o_empty[ob]);
-      if (starts && !ends) {
-        const DecodeSplit sp(total, nc);
-        const int c = static_cast<int>(blockIdx.x);
-        mt = make_int4(wk.b, wk.h * p.G + g0, sp.owner(sp.begin(c + 1) + (wk.n - run) - 1) - c + 1, 0);
-      }
+      const int cost = C::kItemCost + C::kTileCost * wk.n;
+      if (starts && !ends) mt = make_int4(wk.b, wk.h * p.G + g0, DecodeSplit(total, nc).owner(x0 + cost - 1) - c + 1, 0);
+      if (ends) x0 += cost;
       wk.advance(p, run);
     }
+    // A share without a tile may still lie inside an item: an empty part.
+    if (warp == C::kEpilogue && c < nc && share[10] == share[11] && lane < GB) p.part_ml[2 * c * GB + lane] = make_float2(-INFINITY, 0.f);
     if (warp == C::kEpilogue && lane == 0) p.meta[blockIdx.x] = mt;
     __syncwarp();
   }
@@ -1119,51 +1191,69 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
 }
 
 // Joins the parts of one item for query head blockIdx.y of its block: CTA c's item starts
-// in c (its second slot) and goes on in the first slots of CTAs c + 1 ...  The parts' sums
-// are added in order, in kThreads / D interleaved groups that are then added in order too.
+// in c (its second slot) and goes on in the first slots of CTAs c + 1 ...  A part of weight 0
+// may be empty and is not read into the sum.  The order of every sum is fixed by the number
+// of parts.  Two dependent loads deep (which item, then its parts) and one barrier: the
+// kernel's time is its latency.
 constexpr int kJoinThreads = 256;
 
 template <int D, int GB>
 __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int kGroups = kJoinThreads / D;
-  __shared__ float wgt[kDecodeMaxCtas], red[kJoinThreads / 32], part[kGroups][D];
+  constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;  // four features a thread, a part a group
+  __shared__ float4 part[kGroups][kCols];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 mt = p.meta[blockIdx.x];
-  const int g = blockIdx.y;
+  const int c = static_cast<int>(blockIdx.x), g = static_cast<int>(blockIdx.y);
+  const int4 mt = p.meta[c];
   if (mt.z == 0 || mt.y % p.G + g >= p.G) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto slot = [&](int i) { return i == 0 ? 2 * static_cast<int>(blockIdx.x) + 1 : 2 * (static_cast<int>(blockIdx.x) + i); };
-  // Weights 2^(m_i - M) of the parts, and the total of l.
-  float M = -INFINITY;
-  for (int i = tid; i < mt.z; i += kJoinThreads) M = fmaxf(M, p.part_ml[slot(i) * GB + g].x);
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[warp] = M;
-  __syncthreads();
-  M = red[0];
-  for (int w = 1; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
-  __syncthreads();
-  float L = 0.f;
-  for (int i = tid; i < mt.z; i += kJoinThreads) {
-    const float2 ml = p.part_ml[slot(i) * GB + g];
-    const float w = ex2(ml.x - M);
-    wgt[i] = w;
-    L += w * ml.y;
+  const int tid = threadIdx.x, lane = tid & 31, col = tid % kCols, grp = tid / kCols;
+  auto row = [&](int i) { return static_cast<long long>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * GB + g; };
+  auto ml_of = [&](int i) { return i < mt.z ? p.part_ml[row(i)] : make_float2(-INFINITY, 0.f); };
+  auto o_of = [&](int i) {
+    return i < mt.z ? *reinterpret_cast<const float4 *>(p.part_o + row(i) * D + 4 * col) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  const float2 ml0 = ml_of(lane);
+  float2 mine = ml_of(grp);
+  float4 o = o_of(grp);
+  // Every warp takes the parts' maximum and sum for itself.
+  float M = ml0.x;
+  for (int i = lane + 32; i < mt.z; i += 32) M = fmaxf(M, ml_of(i).x);
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+  float L = ml0.y * ex2(ml0.x - M);
+  for (int i = lane + 32; i < mt.z; i += 32) {
+    const float2 ml = ml_of(i);
+    L += ml.y * ex2(ml.x - M);
   }
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (lane == 0) red[warp] = L;
-  __syncthreads();
-  L = red[0];
-  for (int w = 1; w < kJoinThreads / 32; ++w) L += red[w];
-  const int f = tid % D, grp = tid / D;
-  float acc = 0.f;
-  for (int i = grp; i < mt.z; i += kGroups) acc += wgt[i] * p.part_o[(static_cast<long long>(slot(i)) * GB + g) * D + f];
-  part[grp][f] = acc;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = grp; i < mt.z; i += kGroups) {
+    const float w = ex2(mine.x - M);
+    if (w != 0.f) {
+      acc.x += w * o.x;
+      acc.y += w * o.y;
+      acc.z += w * o.z;
+      acc.w += w * o.w;
+    }
+    mine = ml_of(i + kGroups);
+    o = o_of(i + kGroups);
+  }
+  part[grp][col] = acc;
   __syncthreads();
   if (grp != 0) return;
-  for (int k = 1; k < kGroups; ++k) acc += part[k][f];
-  const long long row = static_cast<long long>(mt.x) * p.Hq + mt.y + g;
-  p.o[row * D + f] = static_cast<uint16_t>(pack_bf16(acc / L, 0.f));
-  if (f == 0 && p.lse) p.lse[row] = (M + log2f(L)) * 0.69314718055994531f;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) {
+    const float4 a = part[k][col];
+    acc.x += a.x;
+    acc.y += a.y;
+    acc.z += a.z;
+    acc.w += a.w;
+  }
+  const long long out = static_cast<long long>(mt.x) * p.Hq + mt.y + g;
+  const float inv = __fdividef(1.f, L);
+  *reinterpret_cast<uint2 *>(p.o + out * D + 4 * col) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (col == 0 && p.lse) p.lse[out] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace fa
