@@ -343,16 +343,17 @@ def fa_dropout_mask(B: int, H: int, N: int, rate: float, seed: int, offset: int,
 # ------------------------------------------------------------ key/value cache
 CACHE_BF16, CACHE_E4M3 = 0, 1
 _STRIDES2 = struct.Struct("@2q")
-_ZERO6 = (0,) * 6
 
 
 def _check_on(t, name: str, dtype, shape, device: int):
     """Type, device and shape of a tensor whose strides the caller deals with."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != device or not t.is_cuda:
+    if not t.is_cuda or t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -363,35 +364,34 @@ def _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale):
     row elements), and (device, B, H, d)."""
     if not isinstance(k_cache, torch.Tensor) or not isinstance(block_table, torch.Tensor):
         raise TypeError("k_cache and block_table must be torch.Tensor")
-    dt, dev = k_cache.dtype, k_cache.get_device()
-    e4m3 = dt == torch.uint8
-    if not e4m3 and dt != torch.bfloat16:
+    dt, dev, shape, table = k_cache.dtype, k_cache.get_device(), k_cache.shape, block_table.shape
+    if dt is not torch.bfloat16 and dt is not torch.uint8:
         raise TypeError(f"k_cache must be torch.bfloat16 or torch.uint8 (e4m3 codes), got {dt}")
-    if not k_cache.is_cuda:
+    if dev < 0:
         raise ValueError("k_cache must be a CUDA tensor")
-    shape, table = k_cache.shape, block_table.shape
     if len(shape) != 4 or len(table) != 2:
         raise ValueError("k_cache is [pages, H, page_size, d] and block_table [B, max_pages]")
     P, H, page, d = shape
     B, per = table
     _check_on(v_cache, "v_cache", dt, shape, dev)
     _check_on(block_table, "block_table", torch.int32, table, dev)
-    _check_on(seq_lens, "seq_lens", torch.int32, table[:1], dev)
-    ks, vs, bs = k_cache.stride(), v_cache.stride(), block_table.stride()
-    if (d > 1 and (ks[3] != 1 or vs[3] != 1)) or (per > 1 and bs[1] != 1) or (B > 1 and seq_lens.stride(0) != 1):
+    _check_on(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    b0, b1 = block_table.stride()
+    if (d > 1 and (k3 != 1 or v3 != 1)) or (per > 1 and b1 != 1) or (B > 1 and seq_lens.stride(0) != 1):
         raise ValueError("the last dimension of k_cache, v_cache, block_table and seq_lens must be contiguous")
-    scales = (None, None)
-    fs = _ZERO6
-    if e4m3:
-        _check_on(k_scale, "k_scale", torch.float32, shape[:3], dev)
-        _check_on(v_scale, "v_scale", torch.float32, shape[:3], dev)
-        scales = (k_scale.data_ptr(), v_scale.data_ptr())
-        fs = k_scale.stride() + v_scale.stride()
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("k_scale and v_scale belong to a cache of e4m3 codes (torch.uint8)")
-    return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), scales[0] or 0, scales[1] or 0, *ks[:3], *vs[:3],
-                             *fs, block_table.data_ptr(), seq_lens.data_ptr(), bs[0], CACHE_E4M3 if e4m3 else CACHE_BF16,
-                             P, H, page, d, B, per), dev, B, H, d
+    if dt is torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to a cache of e4m3 codes (torch.uint8)")
+        return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), 0, 0, k0, k1, k2, v0, v1, v2, 0, 0, 0, 0, 0, 0,
+                                 block_table.data_ptr(), seq_lens.data_ptr(), b0, CACHE_BF16, P, H, page, d, B,
+                                 per), dev, B, H, d
+    _check_on(k_scale, "k_scale", torch.float32, (P, H, page), dev)
+    _check_on(v_scale, "v_scale", torch.float32, (P, H, page), dev)
+    return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k0, k1, k2,
+                             v0, v1, v2, *k_scale.stride(), *v_scale.stride(), block_table.data_ptr(),
+                             seq_lens.data_ptr(), b0, CACHE_E4M3, P, H, page, d, B, per), dev, B, H, d
 
 
 def _call_on(device: int, where: str, stream, fn, *args) -> None:
@@ -490,9 +490,7 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
         lse_ptr = lse.data_ptr()
-    if not isinstance(workspace, torch.Tensor):
-        raise TypeError("workspace must be a torch.Tensor")
-    _check_on(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _check_on(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
     if not (q.is_contiguous() and o.is_contiguous() and workspace.is_contiguous()):
         raise ValueError("q, o and workspace must be contiguous")
     _call_on(dev, "fa_decode", stream, _lib.fa_decode, c, q.data_ptr(), o.data_ptr(), lse_ptr, Hq, scale, window,

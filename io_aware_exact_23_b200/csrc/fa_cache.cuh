@@ -92,79 +92,145 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
   return __half22float2(__half2(h));
 }
 
+// Both kernels below give a warp `rows` (at most 32) rows of d elements.  Lane i first finds
+// where row i lies (sequence, page, strides: some hundred cycles of dependent loads and 64-bit
+// arithmetic, once per row), then the warp walks over the rows, kLanes lanes to a row with 16
+// bytes of bf16 each, taking the addresses from the lanes that know them.  (With every lane
+// finding its own piece's address, 145 to 245 instructions went into a piece, and writing 8275
+// tokens x 8 heads x 128 as e4m3 took 25 us, reading 32 ragged sequences back 90 us.)
+constexpr int kCacheThreads = 256;
+constexpr int kCacheWarps = kCacheThreads / 32;
+
+template <class T>
+__device__ __forceinline__ T *shfl_ptr(T *p, int lane) {
+  return reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), lane));
+}
+
 // ------------------------------------------------------------------- append
 struct AppendParams {
   CacheView c;
-  const uint16_t *x[2];     // k_new, v_new
+  const uint16_t *x[2];      // k_new, v_new
   long long x_stride[2][2];  // token, head
   const int *cu_new;
   int T;
+  int rows;  // per warp
 };
 
-constexpr int kCacheThreads = 256;
+// q = x / f for a pair, correctly rounded.  Markstein's division (IBM J. Res. Dev. 34(1),
+// 1990): with r = 1 / f correctly rounded and y = x r, the remainder x - y f is exact in a
+// fused multiply-add, and y + (x - y f) r rounds to the quotient.  Only quotients that e4m3
+// can tell from 0 matter (2^-11 and up), whose remainders stay representable for f in
+// [2^-80, 2^100] (and of zeros always); other rows take the division itself.
+__device__ __forceinline__ uint64_t divide2(uint64_t x, uint64_t f, uint64_t r) {
+  uint64_t y;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(r));
+  const uint64_t ny = y ^ 0x8000000080000000ull;
+  return ffma2(ffma2(ny, f, x), r, y);
+}
 
-// One thread per 16-byte chunk of an input row; rows (token, K or V, head), head
-// fastest, so that neighbouring threads read neighbouring memory.
+// Rows are (token, K or V, head), head fastest.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const AppendParams p) {
-  constexpr int kLanes = D / 8;  // threads per row
+__global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = D / 8;         // lanes per row
+  constexpr int kAtOnce = 32 / kLanes;  // rows per pass
+  constexpr int kBatch = 4;             // passes in flight
   const CacheView &c = p.c;
-  const long long i = static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
-  const long long vec = i / kLanes;
-  const int chunk = static_cast<int>(i % kLanes);
-  const long long row2 = vec / c.H;
-  const int h = static_cast<int>(vec % c.H);
-  const int t = static_cast<int>(row2 >> 1), which = static_cast<int>(row2 & 1);
-  int b = t, pos = -1;
-  bool live = t < p.T;
-  if (live) {
+  const int lane = threadIdx.x & 31;
+  const long long total = 2ll * p.T * c.H;
+  const long long r0 = (static_cast<long long>(blockIdx.x) * kCacheWarps + (threadIdx.x >> 5)) * p.rows;
+  if (r0 >= total) return;
+  const int rows = static_cast<int>(total - r0 < p.rows ? total - r0 : p.rows);
+  const uint16_t *src = nullptr;
+  uint8_t *dst = nullptr;
+  float *fdst = nullptr;
+  if (lane < rows) {
+    const unsigned r = static_cast<unsigned>(r0) + lane, vec = r / static_cast<unsigned>(c.H);
+    const int h = static_cast<int>(r - vec * c.H), t = static_cast<int>(vec >> 1), which = static_cast<int>(vec & 1);
+    int b = t, pos = -1;
     if (p.cu_new == nullptr) {
       pos = cache_len(c, b, kKernelAppend) - 1;
+    } else if (t < __ldg(p.cu_new + c.B)) {
+      int lo = 0, hi = c.B;  // cu_new[lo] <= t < cu_new[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.cu_new + mid) <= t)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      b = lo;
+      pos = cache_len(c, b, kKernelAppend) - (__ldg(p.cu_new + b + 1) - t);
+    }
+    int row = 0;
+    const int page = pos >= 0 ? cache_page(c, b, pos, row, kKernelAppend) : -1;
+    if (page >= 0) {
+      src = p.x[which] + t * p.x_stride[which][0] + h * p.x_stride[which][1];
+      const long long off = page * c.stride[which][0] + h * c.stride[which][1] + row * c.stride[which][2];
+      dst = c.kv[which] + off * (E4M3 ? 1 : 2);
+      if constexpr (E4M3)
+        fdst = c.scale[which] + (page * c.scale_stride[which][0] + h * c.scale_stride[which][1] +
+                                 row * c.scale_stride[which][2]);
+    }
+  }
+  const int chunk = lane % kLanes, sub = lane / kLanes;
+  float mine = 0.f;  // lane i: row i's factor
+  for (int q0 = 0; q0 < rows; q0 += kBatch * kAtOnce) {
+    uint4 w[kBatch];
+    uint8_t *to[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int q = q0 + k * kAtOnce + sub;
+      const uint16_t *from = shfl_ptr(src, q & 31);
+      to[k] = shfl_ptr(dst, q & 31);
+      if (q >= rows) to[k] = nullptr;
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (to[k]) w[k] = __ldg(reinterpret_cast<const uint4 *>(from) + chunk);
+    }
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (to[k]) reinterpret_cast<uint4 *>(to[k])[chunk] = w[k];
     } else {
-      // The sequence whose tokens hold t: the last b with cu_new[b] <= t.
-      int lo = 0, hi = c.B;  // cu_new[lo] <= t < cu_new[hi], if t is a token at all
-      live = t < __ldg(p.cu_new + c.B);
-      if (live) {
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(p.cu_new + mid) <= t)
-            lo = mid;
-          else
-            hi = mid;
+      // The rows' largest magnitudes, as bf16 bits (a NaN is above all), brought to the rows'
+      // lanes: lane q - q0 makes the factor of row q and its reciprocal, once for the row.
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        uint32_t m2 = __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu),
+                               __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu));
+        m2 = max(m2 >> 16, m2 & 0xffffu);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+        const uint32_t its = __shfl_sync(0xffffffffu, m2, (lane % kAtOnce) * kLanes);
+        if (lane / kAtOnce == k) top = its;
+      }
+      const float f = __fdiv_rn(max_nan(__uint_as_float(top << 16), 1e-30f), 448.f);
+      const float r = (f >= 0x1p-80f && f <= 0x1p100f) || top == 0 ? __frcp_rn(f) : 0.f;  // 0: divide
+      const float back = __shfl_sync(0xffffffffu, f, (lane - q0) & 31);
+      if (lane >= q0 && lane < q0 + kBatch * kAtOnce) mine = back;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k * kAtOnce + sub), rk = __shfl_sync(0xffffffffu, r, k * kAtOnce + sub);
+        const uint64_t f2 = f2pack(fk, fk), r2 = f2pack(rk, rk);
+        const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        float a[8];
+        if (rk != 0.f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f2unpack(divide2(f2pack(bf16_lo(words[e]), bf16_hi(words[e])), f2, r2), a[2 * e], a[2 * e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[2 * e] = __fdiv_rn(bf16_lo(words[e]), fk);
+            a[2 * e + 1] = __fdiv_rn(bf16_hi(words[e]), fk);
+          }
         }
-        b = lo;
-        pos = cache_len(c, b, kKernelAppend) - (__ldg(p.cu_new + b + 1) - t);
+        if (to[k])
+          reinterpret_cast<uint2 *>(to[k])[chunk] =
+              make_uint2(pack_e4m3x4(a[0], a[1], a[2], a[3]), pack_e4m3x4(a[4], a[5], a[6], a[7]));
       }
     }
-    live = live && pos >= 0;
   }
-  int row = 0, page = -1;
-  if (live) page = cache_page(c, b, pos, row, kKernelAppend);
-  live = page >= 0;
-  uint4 w = make_uint4(0u, 0u, 0u, 0u);
-  if (live)
-    w = *reinterpret_cast<const uint4 *>(p.x[which] + t * p.x_stride[which][0] + h * p.x_stride[which][1] + chunk * 8);
-  const long long off = page * c.stride[which][0] + h * c.stride[which][1] + row * c.stride[which][2] + chunk * 8;
-  if constexpr (!E4M3) {
-    if (live) *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(c.kv[which]) + off) = w;
-  } else {
-    const float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
-                        bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-    float m = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float f = __fdiv_rn(max_nan(m, 1e-30f), 448.f);
-    if (live) {
-      const uint32_t lo = pack_e4m3x4(__fdiv_rn(x[0], f), __fdiv_rn(x[1], f), __fdiv_rn(x[2], f), __fdiv_rn(x[3], f));
-      const uint32_t hi = pack_e4m3x4(__fdiv_rn(x[4], f), __fdiv_rn(x[5], f), __fdiv_rn(x[6], f), __fdiv_rn(x[7], f));
-      *reinterpret_cast<uint2 *>(c.kv[which] + off) = make_uint2(lo, hi);
-      if (chunk == 0)
-        c.scale[which][page * c.scale_stride[which][0] + h * c.scale_stride[which][1] +
-                       row * c.scale_stride[which][2]] = f;
-    }
-  }
+  if (E4M3 && fdst) *fdst = mine;
 }
 
 // ------------------------------------------------------------------- gather
@@ -172,44 +238,77 @@ struct GatherParams {
   CacheView c;
   uint16_t *out[2];  // k_out, v_out [B, H * rep, N, d], or null
   int rep, N;
+  int rows, parts;  // rows per warp, and warps per sequence and head
 };
 
-// One thread per 16-byte chunk of an output row of the cache's heads; the value is
+// A warp writes the rows [part * rows, ...) of one (sequence, cache head, K or V); heads are
+// the warps' fastest index: the heads of a token may be neighbours in the cache.  A row is
 // read once and stored rep times.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const GatherParams p) {
-  constexpr int kLanes = D / 8;
+__global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const __grid_constant__ GatherParams p) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
   const CacheView &c = p.c;
-  const int which = blockIdx.y;
-  if (p.out[which] == nullptr) return;
-  const long long i = static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x;
-  const int chunk = static_cast<int>(i % kLanes);
-  const long long r = i / kLanes;
-  const int n = static_cast<int>(r % p.N);
-  const long long bh = r / p.N;
-  if (bh >= static_cast<long long>(c.B) * c.H) return;
-  const int b = static_cast<int>(bh / c.H), h = static_cast<int>(bh % c.H);
-  uint4 w = make_uint4(0u, 0u, 0u, 0u);
-  if (n < cache_len(c, b, kKernelGather)) {
-    int row = 0;
-    const int page = cache_page(c, b, n, row, kKernelGather);
-    if (page >= 0) {
-      const long long off = page * c.stride[which][0] + h * c.stride[which][1] + row * c.stride[which][2] + chunk * 8;
-      if constexpr (!E4M3) {
-        w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(c.kv[which]) + off);
+  const int which = blockIdx.y, lane = threadIdx.x & 31;
+  uint16_t *out = p.out[which];
+  const unsigned unit = blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
+  if (out == nullptr || unit >= static_cast<unsigned>(c.B) * c.H * p.parts) return;
+  const unsigned run = unit / static_cast<unsigned>(c.H);
+  const int h = static_cast<int>(unit - run * c.H), b = static_cast<int>(run / static_cast<unsigned>(p.parts));
+  const int n0 = static_cast<int>(run - static_cast<unsigned>(b) * p.parts) * p.rows;
+  const int rows = min(p.rows, p.N - n0);
+  // Lane i's row; its page id is read beside the length it depends on (the table has it in any case).
+  const uint8_t *src = nullptr;
+  float f = 0.f;
+  {
+    const int n = n0 + lane, pi = cache_page_index(c, n);
+    const int page = lane < rows && n < c.cap ? __ldg(c.block_table + b * c.bt_stride + pi) : -1;
+    if (lane < rows && n < cache_len(c, b, kKernelGather)) {
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_pages)) {
+        record_cache_error(c.status, kKernelGather, b, c.seq);
       } else {
-        const float f = c.scale[which][page * c.scale_stride[which][0] + h * c.scale_stride[which][1] +
-                                       row * c.scale_stride[which][2]];
-        const uint2 q = *reinterpret_cast<const uint2 *>(c.kv[which] + off);
-        const float2 a0 = e4m3x2_to_float2(static_cast<uint16_t>(q.x)), a1 = e4m3x2_to_float2(static_cast<uint16_t>(q.x >> 16));
-        const float2 a2 = e4m3x2_to_float2(static_cast<uint16_t>(q.y)), a3 = e4m3x2_to_float2(static_cast<uint16_t>(q.y >> 16));
-        w = make_uint4(pack_bf16(a0.x * f, a0.y * f), pack_bf16(a1.x * f, a1.y * f), pack_bf16(a2.x * f, a2.y * f),
-                       pack_bf16(a3.x * f, a3.y * f));
+        const int row = n - pi * c.page_size;
+        src = c.kv[which] + (page * c.stride[which][0] + h * c.stride[which][1] + row * c.stride[which][2]) * (E4M3 ? 1 : 2);
+        if constexpr (E4M3)
+          f = __ldg(c.scale[which] + (page * c.scale_stride[which][0] + h * c.scale_stride[which][1] +
+                                      row * c.scale_stride[which][2]));
       }
     }
   }
-  uint16_t *out = p.out[which] + (bh * p.rep * p.N + n) * D + chunk * 8;
-  for (int k = 0; k < p.rep; ++k, out += static_cast<long long>(p.N) * D) *reinterpret_cast<uint4 *>(out) = w;
+  const int chunk = lane % kLanes, sub = lane / kLanes;
+  out += ((static_cast<long long>(b) * c.H + h) * p.rep * p.N + n0) * D;
+  const long long next = static_cast<long long>(p.N) * D;  // to the same row of the next repeat
+  for (int q0 = 0; q0 < rows; q0 += kBatch * kAtOnce) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const uint8_t *from = shfl_ptr(src, (q0 + k * kAtOnce + sub) & 31);
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (from && q0 + k * kAtOnce + sub < rows) {
+        if constexpr (!E4M3) {
+          w[k] = __ldg(reinterpret_cast<const uint4 *>(from) + chunk);
+        } else {
+          const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(from) + chunk);
+          w[k].x = codes.x;
+          w[k].y = codes.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int q = q0 + k * kAtOnce + sub;
+      if constexpr (E4M3) {
+        const float s = __shfl_sync(0xffffffffu, f, q & 31);
+        const float2 a0 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].x)), a1 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].x >> 16));
+        const float2 a2 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].y)), a3 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].y >> 16));
+        w[k] = make_uint4(pack_bf16(a0.x * s, a0.y * s), pack_bf16(a1.x * s, a1.y * s), pack_bf16(a2.x * s, a2.y * s),
+                          pack_bf16(a3.x * s, a3.y * s));
+      }
+      if (q < rows) {
+        uint16_t *at = out + q * D + chunk * 8;
+        for (int r = 0; r < p.rep; ++r, at += next) *reinterpret_cast<uint4 *>(at) = w[k];
+      }
+    }
+  }
 }
 
 }  // namespace fa

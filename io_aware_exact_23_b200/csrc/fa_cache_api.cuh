@@ -81,10 +81,18 @@ int make_view(const fa_paged_cache *c, fa::CacheView *v, DeviceState **ds) {
   return FA_OK;
 }
 
-// Blocks of kCacheThreads for n threads, or 0 if there are more than a grid holds.
-unsigned blocks_for(long long n) {
-  const long long g = (n + fa::kCacheThreads - 1) / fa::kCacheThreads;
-  return g > 0x7fffffffll ? 0u : static_cast<unsigned>(g);
+// Rows of a warp of the append and gather kernels, in passes of 256 / d: eight passes, so that
+// most lanes find a row's address, but four (one round of loads) where eight would leave fewer
+// than 16 warps per SM.  8275 tokens x 8 heads x 128 written as e4m3 in passes of 8 / 4: 16.6 /
+// 18.6 us; 300 tokens x 8 heads x 128 read back four times: 3.9 / 3.6 us.
+int rows_per_warp(long long rows, int d, int num_sms) {
+  const int pass = 256 / d;
+  return rows >= 8ll * pass * 16 * num_sms ? 8 * pass : 4 * pass;
+}
+
+unsigned blocks_for(long long rows, int per_warp) {
+  const long long warps = (rows + per_warp - 1) / per_warp;
+  return static_cast<unsigned>((warps + fa::kCacheWarps - 1) / fa::kCacheWarps);
 }
 
 // K or V as the 4-D tensor (feature, row of the page, head, page) that the decode kernel
@@ -191,8 +199,10 @@ int fa_cache_append(const fa_paged_cache *cache, const void *k_new, const void *
   p.x[1] = static_cast<const uint16_t *>(v_new);
   p.cu_new = cu_new;
   p.T = T;
-  const unsigned grid = blocks_for(2ll * T * cache->H * (cache->d / 8));
-  if (grid == 0) return FA_ERR_UNSUPPORTED;
+  const long long total = 2ll * T * cache->H;
+  if (total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  p.rows = rows_per_warp(total, cache->d, ds->num_sms);
+  const unsigned grid = blocks_for(total, p.rows);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == FA_CACHE_E4M3;
   if (cache->d == 64) {
@@ -224,7 +234,10 @@ int fa_cache_gather(const fa_paged_cache *cache, void *k_out, void *v_out, int r
   p.out[1] = static_cast<uint16_t *>(v_out);
   p.rep = rep;
   p.N = N;
-  const dim3 grid(blocks_for(static_cast<long long>(cache->B) * cache->H * N * (cache->d / 8)), 2);
+  const long long heads = static_cast<long long>(cache->B) * cache->H;
+  p.rows = rows_per_warp(heads * N, cache->d, ds->num_sms);
+  p.parts = (N - 1) / p.rows + 1;
+  const dim3 grid(blocks_for(heads * p.parts, 1), 2);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == FA_CACHE_E4M3;
   if (cache->d == 64) {
