@@ -18,6 +18,12 @@ namespace fa {
 enum : int { kStatusCache = 9 };
 enum : int { kKernelAppend = 6, kKernelGather = 7, kKernelDecode = 8 };
 
+// Programmatic dependent launch.  The cache's kernels are launched so that they may start while
+// the stream's previous kernel ends: a kernel lets the next one come at once (pdl_launch) and
+// touches no memory that is not its own before the previous one is complete (pdl_wait).
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The cache as the kernels see it (include/fa_cache.h describes the fields).
 struct CacheView {
   uint8_t *kv[2];        // K, V base addresses
@@ -134,6 +140,8 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const __
   constexpr int kLanes = D / 8;         // lanes per row
   constexpr int kAtOnce = 32 / kLanes;  // rows per pass
   constexpr int kBatch = 4;             // passes in flight
+  pdl_launch();
+  pdl_wait();
   const CacheView &c = p.c;
   const int lane = threadIdx.x & 31;
   const long long total = 2ll * p.T * c.H;
@@ -247,6 +255,8 @@ struct GatherParams {
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const __grid_constant__ GatherParams p) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
+  pdl_launch();
+  pdl_wait();
   const CacheView &c = p.c;
   const int which = blockIdx.y, lane = threadIdx.x & 31;
   uint16_t *out = p.out[which];

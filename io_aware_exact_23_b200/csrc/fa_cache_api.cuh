@@ -81,6 +81,23 @@ int make_view(const fa_paged_cache *c, fa::CacheView *v, DeviceState **ds) {
   return FA_OK;
 }
 
+// A launch that may begin while the stream's previous kernel ends (pdl_wait in the kernel).
+template <class... Formal, class... Actual>
+cudaError_t launch_early(void (*kernel)(Formal...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const Actual &...args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Rows of a warp of the append and gather kernels, in passes of 256 / d: eight passes, so that
 // most lanes find a row's address, but four (one round of loads) where eight would leave fewer
 // than 16 warps per SM.  8275 tokens x 8 heads x 128 written as e4m3 in passes of 8 / 4: 16.6 /
@@ -144,19 +161,10 @@ cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev);
   }
-  fa::fa_decode_kernel<D, E4M3, GB><<<grid, C::kThreads, C::kSmemBytes, stream>>>(tk, tv, p);
-  e = cudaGetLastError();
+  e = launch_early(fa::fa_decode_kernel<D, E4M3, GB>, dim3(grid), C::kThreads, C::kSmemBytes, stream, tk, tv, p);
   if (e != cudaSuccess || grid == 1) return e;  // one CTA leaves no parts
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, static_cast<unsigned>(p.G < GB ? p.G : GB));
-  cfg.blockDim = dim3(fa::kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa::fa_decode_join_kernel<D, GB>, p);
+  return launch_early(fa::fa_decode_join_kernel<D, GB>, dim3(grid, static_cast<unsigned>(p.G < GB ? p.G : GB)),
+                      fa::kJoinThreads, 0, stream, p);
 }
 
 template <int D, bool E4M3>
@@ -205,18 +213,11 @@ int fa_cache_append(const fa_paged_cache *cache, const void *k_new, const void *
   const unsigned grid = blocks_for(total, p.rows);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == FA_CACHE_E4M3;
-  if (cache->d == 64) {
-    if (e4m3)
-      fa::fa_cache_append_kernel<64, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
-    else
-      fa::fa_cache_append_kernel<64, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
-  } else {
-    if (e4m3)
-      fa::fa_cache_append_kernel<128, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
-    else
-      fa::fa_cache_append_kernel<128, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const auto kernel = cache->d == 64 ? (e4m3 ? fa::fa_cache_append_kernel<64, true> : fa::fa_cache_append_kernel<64, false>)
+                                     : (e4m3 ? fa::fa_cache_append_kernel<128, true> : fa::fa_cache_append_kernel<128, false>);
+  const cudaError_t e = launch_early(kernel, dim3(grid), fa::kCacheThreads, 0, s, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_cache_gather(const fa_paged_cache *cache, void *k_out, void *v_out, int rep, int N, void *stream) {
@@ -240,18 +241,11 @@ int fa_cache_gather(const fa_paged_cache *cache, void *k_out, void *v_out, int r
   const dim3 grid(blocks_for(heads * p.parts, 1), 2);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->type == FA_CACHE_E4M3;
-  if (cache->d == 64) {
-    if (e4m3)
-      fa::fa_cache_gather_kernel<64, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
-    else
-      fa::fa_cache_gather_kernel<64, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
-  } else {
-    if (e4m3)
-      fa::fa_cache_gather_kernel<128, true><<<grid, fa::kCacheThreads, 0, s>>>(p);
-    else
-      fa::fa_cache_gather_kernel<128, false><<<grid, fa::kCacheThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const auto kernel = cache->d == 64 ? (e4m3 ? fa::fa_cache_gather_kernel<64, true> : fa::fa_cache_gather_kernel<64, false>)
+                                     : (e4m3 ? fa::fa_cache_gather_kernel<128, true> : fa::fa_cache_gather_kernel<128, false>);
+  const cudaError_t e = launch_early(kernel, grid, fa::kCacheThreads, 0, s, p);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_decode_workspace_bytes(int B, int Hq, int H, int d) {

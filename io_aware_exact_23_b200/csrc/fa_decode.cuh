@@ -371,6 +371,7 @@ struct DecodeWalk {
 struct DecodePages {
   int b = -1, blk = -1, ids = -1;
   int nb = -1, nblk = -1, nids = -1;
+  bool moved = false;
 
   __device__ __forceinline__ static int load(const CacheView &c, int b, int blk, int len, int first) {
     const int i = 32 * blk + static_cast<int>(lane_id());
@@ -389,7 +390,16 @@ struct DecodePages {
       id = c.num_pages;
     }
     ids = id;
-    // What comes next: the sequence's next block, its first one for the next head, or the
+    moved = true;
+    return pi;
+  }
+  // After a move: ask for what comes next.
+  __device__ __forceinline__ void ahead(const DecodeParams &p, const DecodeWalk &wk) {
+    if (!moved) return;
+    moved = false;
+    const CacheView &c = p.c;
+    const int at = blk;
+    // The sequence's next block, its first one for the next head, or the
     // next sequence's first (as far as the walk holds its length).
     const int home = cache_page_index(c, wk.tile0 << 7) >> 5;
     nb = -1;
@@ -408,7 +418,6 @@ struct DecodePages {
         nids = load(c, nb, nblk, len, first);
       }
     }
-    return pi;
   }
   __device__ __forceinline__ static bool load_needed(const CacheView &c, const DecodeWalk &wk, int at) {
     const int i = 32 * at + static_cast<int>(lane_id());
@@ -455,13 +464,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const WaitCtx ctx{p.c.status, abort_flag, kKernelDecode, p.c.seq};
-  // This thread's first sequence for the share below; the load runs while barriers are set up.
-  const int per = (p.c.B + C::kThreads - 1) / C::kThreads;
-  const int b_lo = min(p.c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.c.B, b_lo + per);
-  const int len_lo = b_lo < b_hi ? __ldg(p.c.seq_lens + b_lo) : 0;
-  // The join kernel may be put on the SMs' leftovers now; it waits for this grid's end.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
+  pdl_launch();
   if (warp == C::kQWarp) {
     if (lane < 2) {
       mbar_init(&bar_q[lane], 32);
@@ -502,11 +505,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
+  pdl_wait();  // nothing before this reads or writes what the stream's earlier kernels may touch
 
   // ---------------------------------------------------------------- the share
   // Thread i counts tiles and cost of sequences [i * per, (i + 1) * per); a scan over the
   // threads gives every share's first sequence.
   {
+    const int per = (p.c.B + C::kThreads - 1) / C::kThreads;
+    const int b_lo = min(p.c.B, static_cast<int>(threadIdx.x) * per), b_hi = min(p.c.B, b_lo + per);
+    const int len_lo = b_lo < b_hi ? __ldg(p.c.seq_lens + b_lo) : 0;
     const int items = p.c.H * p.nblk;
     auto tiles_of = [&](int b) {
       const int raw = b == b_lo ? len_lo : __ldg(p.c.seq_lens + b);
@@ -534,17 +541,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     int2 *sums = reinterpret_cast<int2 *>(smem);  // [kWarps], before anything else is there
     if (lane == 31) sums[warp] = make_int2(it, ic);
     __syncthreads();
-    int total_t = 0, total_c = 0, before_t = it - tiles, before_c = ic - cost;
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-      const int2 v = sums[w];
-      if (w < warp) {
-        before_t += v.x;
-        before_c += v.y;
-      }
-      total_t += v.x;
-      total_c += v.y;
-    }
+    const int2 v = lane < C::kWarps ? sums[lane] : make_int2(0, 0);
+    const int total_t = __reduce_add_sync(0xffffffffu, v.x), total_c = __reduce_add_sync(0xffffffffu, v.y);
+    const int before_t = __reduce_add_sync(0xffffffffu, lane < warp ? v.x : 0) + it - tiles;
+    const int before_c = __reduce_add_sync(0xffffffffu, lane < warp ? v.y : 0) + ic - cost;
     const int nc = min(static_cast<int>(gridDim.x), total_t), c = static_cast<int>(blockIdx.x);
     if (c < nc) {
       const DecodeSplit sp(total_c, nc);
@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           ph ^= 1;
         }
       }
+      pg.ahead(p, wk);
       wk.advance(p, 1);
     }
     // The last loads have landed before the CTA can exit.
@@ -838,6 +839,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         }
         __syncwarp();
         cp_async_arrive(&bar_sc[st]);
+        pg.ahead(p, wk);
         wk.advance(p, 1);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1201,7 +1203,8 @@ template <int D, int GB>
 __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;  // four features a thread, a part a group
   __shared__ float4 part[kGroups][kCols];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch();
+  pdl_wait();
   const int c = static_cast<int>(blockIdx.x), g = static_cast<int>(blockIdx.y);
   const int4 mt = p.meta[c];
   if (mt.z == 0 || mt.y % p.G + g >= p.G) return;
