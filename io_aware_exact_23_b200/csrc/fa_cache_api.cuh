@@ -145,8 +145,8 @@ size_t decode_o_offset(int gb) { return decode_ml_offset() + 2ull * fa::kDecodeM
 size_t decode_bytes(int gb, int d) { return decode_o_offset(gb) + 2ull * fa::kDecodeMaxCtas * gb * d * sizeof(float); }
 
 template <int D, bool E4M3, int GB>
-cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p, int num_sms,
-                          long long most, cudaStream_t stream) {
+cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, fa::DecodeParams p, int num_sms, long long most,
+                          cudaStream_t stream) {
   using C = fa::DecodeCfg<D, E4M3, GB>;
   // As many CTAs as are resident at a time, or one per tile if there can be no more.
   long long ctas = static_cast<long long>(num_sms) * C::kCtas;
@@ -161,9 +161,11 @@ cudaError_t launch_decode(const CUtensorMap &tk, const CUtensorMap &tv, const fa
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev);
   }
+  const long long items = static_cast<long long>(p.c.B) * p.c.H * p.nblk;
+  p.by_item = items < grid;
   e = launch_early(fa::fa_decode_kernel<D, E4M3, GB>, dim3(grid), C::kThreads, C::kSmemBytes, stream, tk, tv, p);
   if (e != cudaSuccess || grid == 1) return e;  // one CTA leaves no parts
-  return launch_early(fa::fa_decode_join_kernel<D, GB>, dim3(grid, static_cast<unsigned>(p.G < GB ? p.G : GB)),
+  return launch_early(fa::fa_decode_join_kernel<D, GB>, dim3(p.by_item ? static_cast<unsigned>(items) : grid, static_cast<unsigned>(p.G < GB ? p.G : GB)),
                       fa::kJoinThreads, 0, stream, p);
 }
 

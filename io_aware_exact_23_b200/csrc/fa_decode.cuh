@@ -24,7 +24,7 @@
 // * e4m3: codes are multiplied as they are (kind::f8f6f4), the factor of K goes into the
 //   score, that of V into the weight.  q (8 bits, scaled by one power of two per 8 heads) is
 //   hi + lo / 16 in e4m3, exact to 2^-20 of its largest element; weights, taken to fp16,
-//   are hi + mid / 16 + lo / 256: 11 bits, and not less than 2^-22 of the largest weight.
+//   are hi + mid / 16 + lo / 256: 11 bits, and not less than 2^-20 of the largest weight.
 // The columns' sums meet again in fp32.
 //
 // Softmax warps.  Four warps own the 128 keys of a tile for 8 query heads, GB / 8 such
@@ -53,7 +53,11 @@ struct DecodeParams {
   int window;         // 0: all positions
   int vec_scales;     // e4m3: four neighbouring tokens' factors are one aligned 16-byte piece
   float scale_log2;   // scale * log2(e)
-  int4 *meta;         // [kDecodeMaxCtas] the item whose parts start at CTA c: {b, first query head, parts, -}; parts 0: none
+  // [kDecodeMaxCtas] items in parts, {b, first query head, parts, first CTA}, parts 0: none.  Entry c
+  // is for the item that begins in CTA c and goes on in the next, or (by_item, where there are
+  // fewer items than CTAs) entry i for item i.
+  int4 *meta;
+  int by_item;
   float2 *part_ml;    // [2 * kDecodeMaxCtas][GB] (m, l) of a part
   float *part_o;      // [2 * kDecodeMaxCtas][GB][d]
 };
@@ -79,8 +83,9 @@ struct DecodeCfg {
   static constexpr int kScStages = 4;  // ring of the keys' factors (e4m3)
   // A score may exceed the running reference by kGrow (log2) before the reference moves;
   // e4m3 weights leave room for it below 448.
-  static constexpr float kGrow = E4M3 ? 3.f : 8.f;
-  static constexpr float kWeight = 32.f;  // e4m3: a weight of 1 is code value 32, 2^kGrow is 256
+  // (With 2^3 instead of 2^5 in e4m3, the first tiles of most segments moved it.)
+  static constexpr float kGrow = E4M3 ? 5.f : 8.f;
+  static constexpr int kWeightLog2 = 3;  // e4m3: a weight of 1 is code value 8, 2^kGrow is 256
 
   static constexpr int kSoftmaxWarps = 4 * kGroups;
   static constexpr int kWarps = kSoftmaxWarps + 8;  // softmax, 4 epilogue, producer, issuer, Q, scales
@@ -424,6 +429,14 @@ struct DecodePages {
     return i >= cache_page_index(c, wk.first) && i <= cache_page_index(c, wk.len - 1);
   }
 };
+
+// Note an item that begins in this CTA for the join kernel: its parts up to the CTA that holds
+// its last unit of cost (0: it is whole).  Out of line: once an item at most.
+__device__ __noinline__ void decode_note(const DecodeParams &p, int b, int h, int blk, int row, int last, int total, int nc) {
+  const int c = static_cast<int>(blockIdx.x);
+  const int parts = last > 0 ? DecodeSplit(total, nc).owner(last) - c + 1 : 0;
+  p.meta[p.by_item ? (b * p.c.H + h) * p.nblk + blk : c] = make_int4(b, row, parts, c);
+}
 
 template <int D, bool E4M3, int GB>
 __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D, E4M3, GB>::kCtas)
@@ -856,7 +869,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     constexpr int kH = C::kHeads, kPairs = kH / 2, kSpan = 32 / kH;  // kSpan lanes end up with one head's maximum
     float *xm = xmax + kH * grp * 4;
     uint64_t nm2[kPairs], l2[kPairs];           // minus the reference, and this key's sum of weights
-    float vref = 1.f, vinv = 1.f;     // e4m3: power of two that V's factors are taken relative to; kWeight / vref
+    float vref = 1.f, vinv = 1.f;     // e4m3: power of two that V's factors are taken relative to; 2^kWeightLog2 / vref
     bool bad = false, stop = false;
     int n = 0, nred = 0, sv = 1;      // tiles, reductions, ring slot of the tile's V
     uint32_t vph = 0;
@@ -976,7 +989,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
               vscale = __uint_as_float(static_cast<uint32_t>(max(static_cast<int>((127u << 23) + old - now), 0)));
             }
             vref = __uint_as_float(now);
-            vinv = __uint_as_float((259u << 23) - now);  // kWeight / now, kWeight = 2^5
+            vinv = __uint_as_float(((254u + C::kWeightLog2) << 23) - now);  // 2^kWeightLog2 / now
           }
           // Head lane / kSpan's maximum; -1e30 stands in for -inf, so that differences stay defined.
           const float4 m4 = *reinterpret_cast<const float4 *>(xr + lane / kSpan * 4);
@@ -1093,7 +1106,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       if (w4 == 0 && lane == 0) {
 #pragma unroll
         for (int g = 0; g < kH; ++g) mstat[ob * GB + kH * grp + g] = -m[g];
-        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = vref * (1.f / C::kWeight);
+        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = vref * (1.f / (1 << C::kWeightLog2));
       }
       __syncwarp();
       if (lane == 0) {
@@ -1111,6 +1124,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
 #pragma unroll 1
     for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
       if (cache_len(p.c, b, kKernelDecode) > 0) continue;
+      if (p.by_item)
+        for (int e = f; e < p.c.H * p.nblk; e += 128) p.meta[b * p.c.H * p.nblk + e] = make_int4(0, 0, 0, 0);
       const long long row0 = static_cast<long long>(b) * p.Hq;
 #pragma unroll 1
       for (int e = f; e < p.Hq * D / 8; e += 128) reinterpret_cast<uint4 *>(p.o + row0 * D)[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -1118,8 +1133,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
 #pragma unroll 1
         for (int e = f; e < p.Hq; e += 128) p.lse[row0 + e] = -INFINITY;
     }
-    // The item that starts in this CTA's last segment and goes on in the next CTA, if any.
-    int4 mt = make_int4(0, 0, 0, 0);
+    if (!p.by_item && f == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     const int total = share[4], nc = share[5], c = static_cast<int>(blockIdx.x);
     int x0 = share[9];  // cost before the walk's item
     bool ok = true;
@@ -1176,13 +1190,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_o_empty[ob]);
       const int cost = C::kItemCost + C::kTileCost * wk.n;
-      if (starts && !ends) mt = make_int4(wk.b, wk.h * p.G + g0, DecodeSplit(total, nc).owner(x0 + cost - 1) - c + 1, 0);
+      if (starts && f == 0 && (p.by_item || !ends))
+        decode_note(p, wk.b, wk.h, wk.blk, wk.h * p.G + g0, ends ? 0 : x0 + cost - 1, total, nc);
       if (ends) x0 += cost;
       wk.advance(p, run);
     }
     // A share without a tile may still lie inside an item: an empty part.
     if (warp == C::kEpilogue && c < nc && share[10] == share[11] && lane < GB) p.part_ml[2 * c * GB + lane] = make_float2(-INFINITY, 0.f);
-    if (warp == C::kEpilogue && lane == 0) p.meta[blockIdx.x] = mt;
     __syncwarp();
   }
 
@@ -1192,8 +1206,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   if (warp == C::kIssuer) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Joins the parts of one item for query head blockIdx.y of its block: CTA c's item starts
-// in c (its second slot) and goes on in the first slots of CTAs c + 1 ...  A part of weight 0
+// Joins the parts of the item of entry blockIdx.x for query head blockIdx.y of its block: it
+// starts in CTA c (its second slot) and goes on in the first slots of CTAs c + 1 ...  A part of weight 0
 // may be empty and is not read into the sum.  The order of every sum is fixed by the number
 // of parts.  Two dependent loads deep (which item, then its parts) and one barrier: the
 // kernel's time is its latency.
@@ -1205,8 +1219,8 @@ __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __gr
   __shared__ float4 part[kGroups][kCols];
   pdl_launch();
   pdl_wait();
-  const int c = static_cast<int>(blockIdx.x), g = static_cast<int>(blockIdx.y);
-  const int4 mt = p.meta[c];
+  const int4 mt = p.meta[blockIdx.x];
+  const int c = mt.w, g = static_cast<int>(blockIdx.y);
   if (mt.z == 0 || mt.y % p.G + g >= p.G) return;
   const int tid = threadIdx.x, lane = tid & 31, col = tid % kCols, grp = tid / kCols;
   auto row = [&](int i) { return static_cast<long long>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * GB + g; };

@@ -101,7 +101,7 @@ def decode_exact(c: Cache, q, scale, window=0, lens=None):
       exponential adds 2^-21, q's scale in the log2 domain 2^-22 |s|;
     * weights go into the product with 16 significant bits (2^-16); for e4m3 values with
       fp16's 11 (2^-11, and 2^-12 for the remainder of three e4m3 parts: 2^-10 holds both)
-      and not below 2^-22 of the largest value; the sums over n keys are in fp32.
+      and not below 2^-20 of the largest value; the sums over n keys are in fp32.
     """
     B, Hq, d = q.shape
     G = Hq // c.H
@@ -128,7 +128,7 @@ def decode_exact(c: Cache, q, scale, window=0, lens=None):
         sums = m * 2.0 ** -23
         do[b] = ((torch.expm1(2 * e) + 2.0 ** (-10 if c.e4m3 else -16) + sums)[..., None] * torch.matmul(p, V.abs())).reshape(Hq, d)
         if c.e4m3:
-            do[b] += (m * 2.0 ** -22 * V.abs().amax((1, 2))[:, None]).expand(c.H, G).reshape(Hq, 1)
+            do[b] += (m * 2.0 ** -20 * V.abs().amax((1, 2))[:, None]).expand(c.H, G).reshape(Hq, 1)
         dl[b] = (e + sums + 2.0 ** -22 * z.abs()).reshape(Hq)
     return o, lse, do, dl
 
