@@ -991,9 +991,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             vref = __uint_as_float(now);
             vinv = __uint_as_float(((254u + C::kWeightLog2) << 23) - now);  // 2^kWeightLog2 / now
           }
-          // Head lane / kSpan's maximum; -1e30 stands in for -inf, so that differences stay defined.
+          // Head lane / kSpan's maximum; the lowest number stands in for -inf, so that differences stay defined.
           const float4 m4 = *reinterpret_cast<const float4 *>(xr + lane / kSpan * 4);
-          const float mc = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -1e30f);
+          const float mc = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -3.402823466e38f);
           float alpha[kH];
 #pragma unroll
           for (int g = 0; g < kPairs; ++g) {
@@ -1122,16 +1122,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     const int f = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
 #pragma unroll 1
-    for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
-      if (cache_len(p.c, b, kKernelDecode) > 0) continue;
-      if (p.by_item)
-        for (int e = f; e < p.c.H * p.nblk; e += 128) p.meta[b * p.c.H * p.nblk + e] = make_int4(0, 0, 0, 0);
-      const long long row0 = static_cast<long long>(b) * p.Hq;
+    for (int at = 0; at < p.c.B; at += 128 * gridDim.x) {
+      const int mine = at + f * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+      uint32_t idle = __ballot_sync(0xffffffffu, mine < p.c.B && __ldg(p.c.seq_lens + mine) <= 0);
+      for (; idle; idle &= idle - 1) {
+        const int b = __shfl_sync(0xffffffffu, mine, __ffs(idle) - 1);
+        const long long row0 = static_cast<long long>(b) * p.Hq;
+        if (p.by_item)
 #pragma unroll 1
-      for (int e = f; e < p.Hq * D / 8; e += 128) reinterpret_cast<uint4 *>(p.o + row0 * D)[e] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse)
+          for (int e = lane; e < p.c.H * p.nblk; e += 32) p.meta[b * p.c.H * p.nblk + e] = make_int4(0, 0, 0, 0);
 #pragma unroll 1
-        for (int e = f; e < p.Hq; e += 128) p.lse[row0 + e] = -INFINITY;
+        for (int e = lane; e < p.Hq * D / 8; e += 32)
+          reinterpret_cast<uint4 *>(p.o + row0 * D)[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse)
+#pragma unroll 1
+          for (int e = lane; e < p.Hq; e += 32) p.lse[row0 + e] = -INFINITY;
+      }
     }
     if (!p.by_item && f == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
     const int total = share[4], nc = share[5], c = static_cast<int>(blockIdx.x);
