@@ -108,6 +108,10 @@ struct DecodeCfg {
   static constexpr int kTailBytes = kScBytes + kMiscFloats * 4 + kFixedBars * 8 + 16 * 4;
   static constexpr int kFit = (kSmemMax - kRingOff - kTailBytes) / (kTileBytes + 16);
   static constexpr int kSlots = kFit > 24 ? 24 : kFit;
+  // How the softmax warps learn, before they rescale O, that the previous tile's V^T P is
+  // complete: its V's slot is free again.  With three slots the slot could be two rounds
+  // further by then, and a barrier of its own (bar_pv) says it.
+  static constexpr bool kPvBar = kSlots < 5;
   static constexpr int kScOff = kRingOff + kSlots * kTileBytes;
   static constexpr int kMiscOff = kScOff + kScBytes;
   static constexpr int kBarOff = kMiscOff + kMiscFloats * 4;
@@ -124,8 +128,8 @@ struct DecodeCfg {
 };
 
 enum DecodeTag : int {
-  kTagDFull = 1, kTagDEmpty = 2, kTagDQ = 3, kTagDQEmpty = 4, kTagDS = 5, kTagDSEmpty = 6, kTagDP = 7, kTagDPEmpty = 8,
-  kTagDO = 9, kTagDOEmpty = 10, kTagDStat = 11, kTagDSc = 12, kTagDScEmpty = 13
+  kTagDFull = 1, kTagDEmpty = 2, kTagDQ = 3, kTagDQEmpty = 4, kTagDS = 5, kTagDP = 6, kTagDPv = 7,
+  kTagDO = 8, kTagDOEmpty = 9, kTagDStat = 10, kTagDSc = 11, kTagDScEmpty = 12
 };
 
 // 4-D tiled load (x = feature, y = row of the page, z = head, w = page).
@@ -160,6 +164,16 @@ __device__ __forceinline__ bool decode_try_wait(uint32_t bar, uint32_t parity) {
       "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// Whether the phase is complete, without suspending.
+__device__ __forceinline__ bool decode_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -448,9 +462,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   uint64_t *bar_q = bars + 0;         // [2] Q of a segment is in shared memory
   uint64_t *bar_q_empty = bars + 2;   // [2] ... and read for the last time
   uint64_t *bar_s = bars + 4;         // [2] S^T of a tile is in tensor memory
-  uint64_t *bar_s_empty = bars + 6;   // [2]
   uint64_t *bar_p = bars + 8;         // [2] P of a tile is in shared memory (V's masked rows are zero, O is rescaled)
-  uint64_t *bar_p_empty = bars + 10;  // [2] the tile's V^T P has completed
+  uint64_t *bar_pv = bars + 10;       // [2] the tile's V^T P has completed (kPvBar)
   uint64_t *bar_o = bars + 12;        // [2] a segment's last V^T P has completed
   uint64_t *bar_o_empty = bars + 14;  // [2] the epilogue has read O and the segment's sums
   uint64_t *bar_stat = bars + 16;     // [2] the segment's m and l are in shared memory
@@ -484,9 +497,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       // The issuer's commit; e4m3: and the softmax warps, for q's scale.
       mbar_init(&bar_q_empty[lane], 1 + (E4M3 ? C::kSoftmaxWarps : 0));
       mbar_init(&bar_s[lane], 1);
-      mbar_init(&bar_s_empty[lane], C::kSoftmaxWarps);
       mbar_init(&bar_p[lane], C::kSoftmaxWarps);
-      mbar_init(&bar_p_empty[lane], 1);
+      mbar_init(&bar_pv[lane], 1);
       mbar_init(&bar_o[lane], 1);
       mbar_init(&bar_o_empty[lane], 4);
       mbar_init(&bar_stat[lane], C::kSoftmaxWarps);
@@ -640,7 +652,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     __syncwarp();
   } else if (warp == C::kIssuer) {
     // --------------------------------------------------------------- issuer
-    // S^T of tile i + 1 goes in ahead of V^T P of tile i, across segments too.
+    // S^T of tile n goes in ahead of V^T P of tile n - 1, across segments too.  That order
+    // stands for barriers: P of tile n - 2 tells that the softmax warps have read S^T of it,
+    // whose columns tile n takes; and S^T of tile n being complete tells them that V^T P of
+    // tile n - 2 is, whose P they overwrite.  The loop is what a CTA's tile takes at least,
+    // and a satisfied wait is some 100 cycles of it.  So V and P, usually both there, are
+    // looked at by two lanes at once (a wait that may suspend must not be: with lanes on
+    // different barriers it sleeps to its limit).
     constexpr uint32_t idesc_s = E4M3 ? make_idesc_e4m3(128, C::kQCols, 0, 0) : make_idesc_bf16(128, C::kQCols, 0, 0);
     constexpr uint32_t idesc_o = E4M3 ? make_idesc_e4m3(128, C::kOCols, 1, 1) : make_idesc_bf16(128, C::kOCols, 1, 1);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -677,7 +695,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       const bool more = wk.rem > 0, ends = wk.run() == 1;
       if (more) {
         if (begins && !(ok = wait(&bar_q[qb], (seg >> 1) & 1, kTagDQ))) break;
-        if (n >= 2 && !(ok = wait(&bar_s_empty[buf], ((n >> 1) - 1) & 1, kTagDSEmpty))) break;
         if (!(ok = wait(&bar_full[s], ph, kTagDFull))) break;
         tc_fence_after();
         const uint64_t kd = sdesc_add(k_desc0, s * C::kTileBytes), qd = sdesc_add(q_desc0, qb * C::kQBytes);
@@ -698,8 +715,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       if (pend_seg >= 0) {  // V^T P of tile n - 1
         const int pb = buf ^ 1, ob = pend_seg & 1;
         if (pend_first && pend_seg >= 2 && !(ok = wait(&bar_o_empty[ob], ((pend_seg >> 1) - 1) & 1, kTagDOEmpty))) break;
-        if (!(ok = wait(&bar_full[pend_s], pend_ph, kTagDFull))) break;
-        if (!(ok = wait(&bar_p[pb], ((n - 1) >> 1) & 1, kTagDP))) break;
+        const uint32_t php = ((n - 1) >> 1) & 1;
+        if (!__all_sync(0xffffffffu, decode_test(lane == 0 ? &bar_full[pend_s] : &bar_p[pb], lane == 0 ? pend_ph : php))) {
+          if (!(ok = wait(&bar_full[pend_s], pend_ph, kTagDFull))) break;
+          if (!(ok = wait(&bar_p[pb], php, kTagDP))) break;
+        }
         tc_fence_after();
         const uint64_t vd = sdesc_add(v_desc0, pend_s * C::kTileBytes), pd = sdesc_add(p_desc0, pb * C::kPBytes);
         const uint32_t to = tm + kOCol0 + ob * C::kOCols;
@@ -713,7 +733,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             mma_ss_w(to, a, b, idesc_o, (!pend_first || ks > 0) ? 1u : 0u);
         }
         mma_commit_w(&bar_empty[pend_s]);
-        mma_commit_w(&bar_p_empty[pb]);
+        if constexpr (C::kPvBar) mma_commit_w(&bar_pv[pb]);
         if (pend_last) mma_commit_w(&bar_o[ob]);
       }
       if (!more) break;
@@ -886,16 +906,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       for (int i = 0; i < run; ++i, ++n) {
         const int buf = n & 1;
         const int pos0 = (wk.tile0 + wk.off + i) * 128;
-        bad |= !decode_wait(ctx, &bar_s[buf], (n >> 1) & 1, kTagDS);
-        if (n >= 2) bad |= !decode_wait(ctx, &bar_p_empty[buf], ((n >> 1) - 1) & 1, kTagDPEmpty);
         float f = qs, fv = 1.f;
-        if constexpr (E4M3) {
+        if constexpr (E4M3) {  // the factors are there first, as a rule
           const int st = n % C::kScStages;
           bad |= !decode_wait(ctx, &bar_sc[st], (n / C::kScStages) & 1, kTagDSc);
           const float *sc = reinterpret_cast<const float *>(smem + C::kScOff + st * 1024);
           f = qs * sc[key];
           fv = sc[128 + key];
         }
+        bad |= !decode_wait(ctx, &bar_s[buf], (n >> 1) & 1, kTagDS);
         __syncwarp();
         tc_fence_after();
         uint64_t v2[kPairs];  // scores before their factor
@@ -907,10 +926,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar_s_empty[buf]);
-            if constexpr (E4M3) mbar_arrive(&bar_sc_empty[n % C::kScStages]);
-          }
+          if (E4M3 && lane == 0) mbar_arrive(&bar_sc_empty[n % C::kScStages]);
 #pragma unroll
           for (int g = 0; g < kPairs; ++g) {
             v2[g] = f2pack(__uint_as_float(hi[2 * g]), __uint_as_float(hi[2 * g + 1]));
@@ -1011,7 +1027,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           }
           if (i > 0) {
             // O holds tiles of this segment on the old reference: bring it to the new one.
-            bad |= !decode_wait(ctx, &bar_p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, kTagDPEmpty);
+            if constexpr (C::kPvBar) {
+              bad |= !decode_wait(ctx, &bar_pv[(n - 1) & 1], ((n - 1) >> 1) & 1, kTagDPv);
+            } else {
+              const int back = sv - 2 + (sv < 2 ? C::kSlots : 0);
+              bad |= !decode_wait(ctx, &bar_empty[back], vph ^ (sv < 2 ? 1u : 0u), kTagDPv);
+            }
             __syncwarp();
             tc_fence_after();
             const uint32_t to = tmem + lane_off + kOCol0 + (seg & 1) * C::kOCols + kH * grp;

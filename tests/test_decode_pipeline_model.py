@@ -48,8 +48,9 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, groups: int = 1, skip:
     empty = [Bar(f"empty{s}", 1) for s in range(slots)]
     pair = lambda nm, c: [Bar(f"{nm}{b}", c) for b in range(2)]  # noqa: E731
     q, q_empty = pair("q", 1), pair("q_empty", 1 + (WARPS if e4m3 else 0))
-    s_full, s_empty = pair("s", 1), pair("s_empty", WARPS)
-    p_full, p_empty = pair("p", WARPS), pair("p_empty", 1)
+    s_full = pair("s", 1)
+    p_full, pv_done = pair("p", WARPS), pair("pv", 1)
+    pv_bar = slots < 5
     o_full, o_empty, stat = pair("o", 1), pair("o_empty", 4), pair("stat", WARPS)
     sc = [Bar(f"sc{s}", 1) for s in range(SCALES)]
     sc_empty = [Bar(f"sc_empty{s}", WARPS) for s in range(SCALES)]
@@ -85,7 +86,8 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, groups: int = 1, skip:
                 reads.update({("O", ob, w): ("O", i, t) for w in range(WARPS)})
             M.mma("mma", reads, {("O", ob, w): ("O", i, t + 1) for w in range(WARPS)})
             M.commit("mma", empty[s])
-            M.commit("mma", p_empty[b])
+            if pv_bar:
+                M.commit("mma", pv_done[b])
             if t in last:
                 M.commit("mma", o_full[ob])
 
@@ -94,8 +96,6 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, groups: int = 1, skip:
             yield lambda: q[i & 1].ready(i >> 1)
             for t in range(n0, n0 + r):
                 s, ph = slot(0, t)
-                if t >= 2:
-                    yield lambda t=t: s_empty[t & 1].ready((t >> 1) - 1)
                 yield lambda s=s, ph=ph: full[s].ready(ph)
                 M.mma("mma", {("slot", s): ("K", t), ("Q", i & 1): ("Q", i)},
                       {("S", t & 1, w): ("S", t) for w in range(WARPS)})
@@ -141,8 +141,6 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, groups: int = 1, skip:
             for t in range(n0, n0 + r):
                 b = t & 1
                 yield lambda t=t, b=b: s_full[b].ready(t >> 1)
-                if t >= 2:
-                    yield lambda t=t, b=b: p_empty[b].ready((t >> 1) - 1)
                 if e4m3:
                     yield lambda t=t: sc[t % SCALES].ready(t // SCALES)
                     M.read(("sc", t % SCALES), ("sc", t))
@@ -153,15 +151,17 @@ def decode_model(runs, slots: int, seed: int, e4m3: bool, groups: int = 1, skip:
                     M.write(("slot", s), v_tag(t))  # each warp its own rows
                 M.read(("S", b, w), ("S", t))
                 yield lambda: True
-                s_empty[b].arrive()
                 if t not in first:
                     yield from agree()
                 if t in first or t in moves[grp]:
                     M.write(("x", (votes >> 1) & 3, w), t)
                     yield from agree()
                 if t in moves[grp]:
-                    if skip != "rescale":
-                        yield lambda t=t: p_empty[(t - 1) & 1].ready((t - 1) >> 1)
+                    if skip != "rescale" and (pv_bar):
+                        yield lambda t=t: pv_done[(t - 1) & 1].ready((t - 1) >> 1)
+                    elif skip != "rescale":
+                        s, ph = slot(1, t - 1)
+                        yield lambda s=s, ph=ph: empty[s].ready(ph)
                     M.read(("O", ob, w), ("O", i, t))
                     M.write(("O", ob, w), ("O", i, t))
                 M.write(("P", b, w), ("P", t))
@@ -214,4 +214,4 @@ def test_model_matches_the_kernel():
     """The rings this model runs are the kernel's (read from its source)."""
     src = open(os.path.join(os.path.dirname(__file__), "..", "io_aware_exact_23_b200", "csrc", "fa_decode.cuh")).read()
     assert int(re.search(r"kScStages = (\d+);", src).group(1)) == SCALES
-    assert "kSlots >= 3" in src and "> 24 ? 24" in src
+    assert "kSlots >= 3" in src and "> 24 ? 24" in src and "kPvBar = kSlots < 5" in src
