@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         bad |= !decode_wait(ctx, &bar_s[buf], (n >> 1) & 1, kTagDS);
         __syncwarp();
         tc_fence_after();
-        uint64_t v2[kPairs];  // scores before their factor
+        uint64_t v2[kPairs];  // scores (before their factor at first)
         {
           const uint32_t ts = tmem + lane_off + buf * C::kQCols + kH * grp;
           uint32_t hi[kH], lo[kH];
@@ -960,12 +960,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           }
           __syncwarp();
         }
-        const uint64_t f2 = f2pack(f, f);
+        // Scores in the log2 domain, rounded once here: a fused multiply-subtract below would be
+        // off from the maximum by the rounding of a product, however large that is.
+#pragma unroll
+        for (int g = 0; g < kPairs; ++g) v2[g] = fmul2(v2[g], f2pack(f, f));
         float x[kH];  // log2 of the weights
         bool grow = true;
         if (i > 0) {
 #pragma unroll
-          for (int g = 0; g < kPairs; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
+          for (int g = 0; g < kPairs; ++g) f2unpack(fadd2(v2[g], nm2[g]), x[2 * g], x[2 * g + 1]);
           float top = x[0];
 #pragma unroll
           for (int g = 1; g < kH; ++g) top = fmaxf(top, x[g]);
@@ -980,7 +983,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           ++nred;
           float v[kH];
 #pragma unroll
-          for (int g = 0; g < kPairs; ++g) f2unpack(fmul2(v2[g], f2), v[2 * g], v[2 * g + 1]);
+          for (int g = 0; g < kPairs; ++g) f2unpack(v2[g], v[2 * g], v[2 * g + 1]);
           reduce_columns<kH>(v, [](float a, float b) { return fmaxf(a, b); });
           if (lane % kSpan == 0) xr[lane / kSpan * 4 + w4] = v[0];
           if constexpr (E4M3) {
@@ -1049,7 +1052,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             tc_fence_before();
           }
 #pragma unroll
-          for (int g = 0; g < kPairs; ++g) f2unpack(ffma2(v2[g], f2, nm2[g]), x[2 * g], x[2 * g + 1]);
+          for (int g = 0; g < kPairs; ++g) f2unpack(fadd2(v2[g], nm2[g]), x[2 * g], x[2 * g + 1]);
         }
         // Weights into P: row = key, this group's heads of each part.
         const uint32_t pb = smem_u32(smem + C::kPOff) + buf * C::kPBytes;

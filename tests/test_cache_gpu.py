@@ -509,3 +509,170 @@ def test_binding_refusals():
         with pytest.raises((TypeError, ValueError)):
             fa.fa_cache_gather(**a)
     ok()
+
+
+# ------------------------------------------------------- calls in other settings
+CAPTURE_FIRST = """
+import math, sys
+sys.path[:0] = [{tests!r}, {root!r}]
+import torch
+from cache_helpers import Cache, check_decode, decode_exact, DEV
+from io_aware_exact_23_b200 import binding as fa
+fa.fa_device_status()  # the device's first call
+for e4m3, Hq, d in ((False, 2, 64), (True, 40, 128)):
+    c = Cache([300, 0, 129], 1, d, 16, e4m3, seed=60)
+    q = torch.randn(3, Hq, d, device=DEV).to(torch.bfloat16)
+    new = torch.randn(3, 1, d, device=DEV).to(torch.bfloat16)
+    o, L = torch.empty_like(q), torch.empty(3, Hq, device=DEV)
+    out = torch.empty(3, Hq, 300, d, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(3, Hq, 1, d), dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.fa_cache_append(new, new, c.k, c.v, **c.args)
+        fa.fa_decode(q, c.k, c.v, o=o, lse=L, scale=0.1, workspace=ws, **c.args)
+        fa.fa_cache_gather(c.k, c.v, k_out=out, v_out=None, **c.args)
+    for _ in range(3):
+        o.fill_(float("nan"))
+        g.replay()
+    assert fa.fa_device_status() == 0
+    check_decode(o, L, decode_exact(c, q, 0.1))
+    ref = c.rows("k", 0, 300)
+    assert ((out[0, 0].double() - ref[0]).abs() <= 2.0 ** -8 * ref[0].abs()).all()
+print("captured")
+"""
+
+
+def test_captured_before_any_other_call_of_its_kind():
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = CAPTURE_FIRST.format(tests=tests, root=os.path.dirname(tests))
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "captured" in got.stdout, got.stderr[-2000:]
+
+
+def test_two_graphs_at_once_with_a_workspace_each():
+    q = [make_q(2, 8, 128, seed=s) for s in (1, 2)]
+    c = [Cache([2500, 700], 2, 128, 16, e, seed=61 + e) for e in (False, True)]
+    res, graphs = [], []
+    for i in range(2):
+        res.append(decode(c[i], q[i]))
+        ws = torch.empty(fa.fa_decode_workspace_bytes(2, 8, 2, 128), dtype=torch.uint8, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(8):
+                decode(c[i], q[i], ws=ws, out=res[i][0])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    ok()
+    for i in range(2):
+        check_decode(*res[i], decode_exact(c[i], q[i], 1 / math.sqrt(128)))
+
+
+def test_decode_from_two_threads():
+    import threading
+    c = [Cache([900, 31, 400], 2, 64, 32, e, seed=63 + e) for e in (False, True)]
+    q = [make_q(3, 4, 64, seed=s) for s in (3, 4)]
+    res, errors = [None, None], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(30):
+                    res[i] = decode(c[i], q[i])
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    ok()
+    for i in range(2):
+        check_decode(*res[i], decode_exact(c[i], q[i], 1 / 8))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_thousands_of_idle_slots(e4m3):
+    """A padded batch of which only a few slots are taken."""
+    lens = [0] * 5000
+    for b in (0, 31, 32, 383, 384, 385, 2999, 4999):
+        lens[b] = 7 + b % 300
+    c = Cache(lens, 1, 64, 16, e4m3, seed=65)
+    run_decode(c, make_q(5000, 1, 64))
+
+
+def test_decode_window_larger_than_any_length():
+    c = Cache([300, 1, 0], 2, 64, 16, False, seed=66)
+    q = make_q(3, 4, 64)
+    a, b = run_decode(c, q, window=2 ** 31 - 1), run_decode(c, q)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_decode_the_same_page_twice():
+    """One sequence whose table names a page twice."""
+    c = Cache([64, 64], 2, 64, 16, False, seed=67)
+    c.table[0, 2] = c.table[0, 0]
+    run_decode(c, make_q(2, 4, 64))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_follows_an_append_without_a_wait(e4m3):
+    """Each kernel may start while the one before it ends: many short steps in a row."""
+    steps, B, H, d = 60, 5, 2, 128
+    c = Cache([steps + 130] * B, H, d, 16, e4m3, seed=68)  # room for the longest one's steps
+    c.lens.copy_(torch.tensor([70, 1, 0, 127, 128 - steps // 2], dtype=torch.int32))
+    q = make_q(B, 8, d, seed=5)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(B, 8, H, d), dtype=torch.uint8, device=DEV)
+    news = torch.randn(steps, 2, B, H, d, device=DEV).to(torch.bfloat16)
+    outs, lens = [], []
+    torch.cuda.synchronize()
+    for t in range(steps):
+        c.lens += 1
+        lens.append(c.lens.clone())
+        fa.fa_cache_append(news[t, 0], news[t, 1], c.k, c.v, **c.args)
+        outs.append(decode(c, q, ws=ws))
+    ok()
+    # Appends only write behind what earlier steps saw: every step can be checked now.
+    for t in range(0, steps, 7):
+        check_decode(*outs[t], decode_exact(c, q, 1 / math.sqrt(d), lens=lens[t].tolist()), f"step {t}")
+
+
+def test_decode_scores_of_no_finite_value():
+    """A row whose every score is the lowest there is (-inf from infinite keys) next to others."""
+    c = Cache([200, 200], 1, 64, 16, False, seed=69)
+    page, off = c.where(0, torch.tensor([3], device=DEV))
+    c.k[page[0], 0, off[0], :] = 0
+    c.k[page[0], 0, off[0], 0] = -float("inf")
+    q = make_q(2, 2, 64).abs()  # every product with that element is -inf
+    run_decode(c, q)  # the key has weight 0, as in the definition
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_very_low_scores(d):
+    """Scores around -1e30: the maximum is far below where it starts from."""
+    c = Cache([300], 1, d, 16, False, seed=70)
+    r = torch.zeros(300, 1, d, device=DEV, dtype=torch.bfloat16)
+    r[:, 0, 0] = -1e31
+    r[150:, 0, 0] = -1e30
+    c.put(c.k, c.ks, 0, torch.arange(300, device=DEV), r)
+    q = torch.zeros(1, 4, d, device=DEV, dtype=torch.bfloat16)
+    q[:, :, 0] = 1
+    o, L = decode(c, q, scale=1.0)
+    ok()
+    ref = c.rows("v", 0, 300)[0, 150:].mean(0)
+    assert ((o[0].double() - ref).abs() <= BF16_HALF * ref.abs() + 2.0 ** -12).all()
+    score = float(r[150, 0, 0])  # -1e30 as bf16 holds it
+    assert ((L.double() - score).abs() <= 2.0 ** -22 * abs(score)).all()
