@@ -270,7 +270,7 @@ int fa_decode(const fa_paged_cache *cache, const void *q, void *o, float *lse, i
   const int G = Hq / cache->H, gb = decode_block(G), nblk = (G + gb - 1) / gb;
   const long long item_tiles = (static_cast<long long>(cache->max_pages) * cache->page_size + 127) / 128;
   const long double most = static_cast<long double>(cache->B) * cache->H * nblk * item_tiles;
-  if (most * 8 >= 2147483648.0L) return FA_ERR_UNSUPPORTED;  // kItemCost + kTileCost = 8
+  if (most * 6 >= 2147483648.0L) return FA_ERR_UNSUPPORTED;  // kItemCost + kTileCost = 6
   fa::DecodeParams p;
   DeviceState *ds = nullptr;
   st = make_view(cache, &p.c, &ds);
