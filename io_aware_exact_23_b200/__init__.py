@@ -9,7 +9,7 @@ from here) raises if the library was not built -- there is no CPU fallback.
 from __future__ import annotations
 
 __all__ = ["fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_device_status", "FaError", "fa_cache_append",
-           "fa_cache_gather", "fa_decode", "fa_decode_workspace_bytes"]
+           "fa_cache_gather", "fa_decode", "fa_decode_workspace_bytes", "KVCache"]
 
 
 def __getattr__(name):

@@ -495,3 +495,39 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
         raise ValueError("q, o and workspace must be contiguous")
     _call_on(dev, "fa_decode", stream, _lib.fa_decode, c, q.data_ptr(), o.data_ptr(), lse_ptr, Hq, scale, window,
              workspace.data_ptr(), workspace.numel())
+
+
+class KVCache:
+    """Allocating convenience wrapper of a paged cache: its tensors and the calls on them.
+
+    The caller owns the pages' allocation: ``block_table`` [B, max_pages] and ``seq_lens``
+    [B] (int32, the cache's device) go with every call.
+    """
+
+    def __init__(self, num_pages: int, H: int, page_size: int, d: int, e4m3: bool = False, device="cuda"):
+        shape = (num_pages, H, page_size, d)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else torch.bfloat16, device=device)
+                          for _ in range(2))
+        self.k_scale = self.v_scale = None
+        if e4m3:
+            self.k_scale, self.v_scale = (torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+
+    def append(self, k_new, v_new, block_table, seq_lens, cu_new=None, stream=None) -> None:
+        fa_cache_append(k_new, v_new, self.k, self.v, block_table, seq_lens, cu_new, self.k_scale, self.v_scale, stream)
+
+    def decode(self, q, block_table, seq_lens, scale: float, window: int = 0):
+        """Returns (o, lse)."""
+        B, Hq, d = q.shape
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        ws = torch.empty(fa_decode_workspace_bytes(B, Hq, self.k.shape[1], d), dtype=torch.uint8, device=q.device)
+        fa_decode(q, self.k, self.v, block_table, seq_lens, o, lse, scale, ws, self.k_scale, self.v_scale, window)
+        return o, lse
+
+    def gather(self, block_table, seq_lens, N: int, rep: int = 1):
+        """Returns (k, v), each [B, H * rep, N, d] bf16."""
+        _, H, _, d = self.k.shape
+        k, v = (torch.empty((block_table.shape[0], H * rep, N, d), dtype=torch.bfloat16, device=self.k.device)
+                for _ in range(2))
+        fa_cache_gather(self.k, self.v, block_table, seq_lens, k, v, self.k_scale, self.v_scale)
+        return k, v

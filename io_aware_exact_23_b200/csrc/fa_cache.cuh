@@ -102,8 +102,8 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
 // where row i lies (sequence, page, strides: some hundred cycles of dependent loads and 64-bit
 // arithmetic, once per row), then the warp walks over the rows, kLanes lanes to a row with 16
 // bytes of bf16 each, taking the addresses from the lanes that know them.  (With every lane
-// finding its own piece's address, 145 to 245 instructions went into a piece, and writing 8275
-// tokens x 8 heads x 128 as e4m3 took 25 us, reading 32 ragged sequences back 90 us.)
+// finding its own piece's address, 145 to 245 instructions went into a piece, and the two
+// cases given below took 25 and 90 us.)
 constexpr int kCacheThreads = 256;
 constexpr int kCacheWarps = kCacheThreads / 32;
 
@@ -122,21 +122,27 @@ struct AppendParams {
   int rows;  // per warp
 };
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // q = x / f for a pair, correctly rounded.  Markstein's division (IBM J. Res. Dev. 34(1),
 // 1990): with r = 1 / f correctly rounded and y = x r, the remainder x - y f is exact in a
 // fused multiply-add, and y + (x - y f) r rounds to the quotient.  Only quotients that e4m3
 // can tell from 0 matter (2^-11 and up), whose remainders stay representable for f in
 // [2^-80, 2^100] (and of zeros always); other rows take the division itself.
 __device__ __forceinline__ uint64_t divide2(uint64_t x, uint64_t f, uint64_t r) {
-  uint64_t y;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(r));
-  const uint64_t ny = y ^ 0x8000000080000000ull;
-  return ffma2(ffma2(ny, f, x), r, y);
+  const uint64_t y = mul2(x, r);
+  return ffma2(ffma2(y ^ 0x8000000080000000ull, f, x), r, y);
 }
 
-// Rows are (token, K or V, head), head fastest.
+// Rows are (token, K or V, head), head fastest.  Bound by its instructions: 8275 tokens x 8
+// heads x 128 as e4m3 take 15.0 us, 51 MB at 3.4 TB/s (five or six resident blocks, with fewer
+// registers: 17.1 us).
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kCacheThreads, 4) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 8;         // lanes per row
   constexpr int kAtOnce = 32 / kLanes;  // rows per pass
   constexpr int kBatch = 4;             // passes in flight
@@ -251,9 +257,11 @@ struct GatherParams {
 
 // A warp writes the rows [part * rows, ...) of one (sequence, cache head, K or V); heads are
 // the warps' fastest index: the heads of a token may be neighbours in the cache.  A row is
-// read once and stored rep times.
+// read once and stored rep times.  Bound by the stores: 4 x 4096 positions x 8 heads x 128 of
+// bf16, each stored four times, take 57.3 us (336 MB at 5.9 TB/s), 32 ragged e4m3 sequences x
+// 16 heads x 64 56.2 us (332 MB; with six resident blocks 58.8 us, for bf16 with seven 58.5 us).
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const __grid_constant__ GatherParams p) {
+__global__ void __launch_bounds__(kCacheThreads, E4M3 ? 7 : 6) fa_cache_gather_kernel(const __grid_constant__ GatherParams p) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
   pdl_launch();
   pdl_wait();
@@ -308,10 +316,19 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_gather_kernel(const __
       const int q = q0 + k * kAtOnce + sub;
       if constexpr (E4M3) {
         const float s = __shfl_sync(0xffffffffu, f, q & 31);
-        const float2 a0 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].x)), a1 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].x >> 16));
-        const float2 a2 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].y)), a3 = e4m3x2_to_float2(static_cast<uint16_t>(w[k].y >> 16));
-        w[k] = make_uint4(pack_bf16(a0.x * s, a0.y * s), pack_bf16(a1.x * s, a1.y * s), pack_bf16(a2.x * s, a2.y * s),
-                          pack_bf16(a3.x * s, a3.y * s));
+        if ((w[k].x | w[k].y) != 0) {  // rows behind a sequence's end are zeros already
+          const uint64_t s2 = f2pack(s, s);
+          const uint32_t codes[2] = {w[k].x, w[k].y};
+          uint32_t r[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(codes[e >> 1] >> (16 * (e & 1))));
+            float x, y;
+            f2unpack(mul2(f2pack(a.x, a.y), s2), x, y);
+            r[e] = pack_bf16(x, y);
+          }
+          w[k] = make_uint4(r[0], r[1], r[2], r[3]);
+        }
       }
       if (q < rows) {
         uint16_t *at = out + q * D + chunk * 8;

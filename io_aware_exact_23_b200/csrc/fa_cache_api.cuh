@@ -100,8 +100,8 @@ cudaError_t launch_early(void (*kernel)(Formal...), dim3 grid, int threads, size
 
 // Rows of a warp of the append and gather kernels, in passes of 256 / d: eight passes, so that
 // most lanes find a row's address, but four (one round of loads) where eight would leave fewer
-// than 16 warps per SM.  8275 tokens x 8 heads x 128 written as e4m3 in passes of 8 / 4: 16.6 /
-// 18.6 us; 300 tokens x 8 heads x 128 read back four times: 3.9 / 3.6 us.
+// than 16 warps per SM.  8275 tokens x 8 heads x 128 written as e4m3 with eight / four passes:
+// 16.6 / 18.6 us; 300 positions x 8 heads x 128 read back four times: 3.9 / 3.6 us.
 int rows_per_warp(long long rows, int d, int num_sms) {
   const int pass = 256 / d;
   return rows >= 8ll * pass * 16 * num_sms ? 8 * pass : 4 * pass;

@@ -231,12 +231,6 @@ __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Two fp32 -> fp16x2, fp16x2 -> e4m3x2 (both to nearest even) and e4m3x2 -> fp16x2 (exact).
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -965,7 +959,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         // Scores in the log2 domain, rounded once here: a fused multiply-subtract below would be
         // off from the maximum by the rounding of a product, however large that is.
 #pragma unroll
-        for (int g = 0; g < kPairs; ++g) v2[g] = fmul2(v2[g], f2pack(f, f));
+        for (int g = 0; g < kPairs; ++g) v2[g] = mul2(v2[g], f2pack(f, f));
         float x[kH];  // log2 of the weights
         bool grow = true;
         if (i > 0) {
@@ -1028,7 +1022,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             alpha[2 * g] = ex2(-a - m0);
             alpha[2 * g + 1] = ex2(-b - m1);
             nm2[g] = f2pack(-m0, -m1);
-            if (i > 0) l2[g] = fmul2(l2[g], f2pack(alpha[2 * g], alpha[2 * g + 1]));
+            if (i > 0) l2[g] = mul2(l2[g], f2pack(alpha[2 * g], alpha[2 * g + 1]));
           }
           if (i > 0) {
             // O holds tiles of this segment on the old reference: bring it to the new one.

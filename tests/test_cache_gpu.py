@@ -676,3 +676,59 @@ def test_decode_very_low_scores(d):
     assert ((o[0].double() - ref).abs() <= BF16_HALF * ref.abs() + 2.0 ** -12).all()
     score = float(r[150, 0, 0])  # -1e30 as bf16 holds it
     assert ((L.double() - score).abs() <= 2.0 ** -22 * abs(score)).all()
+
+
+# ------------------------------------------------------------------- wrapper
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_wrapper(e4m3):
+    ref = Cache([90, 0, 33], 2, 64, 16, e4m3, seed=71, fill=False)
+    c = fa.KVCache(ref.num, 2, 16, 64, e4m3)
+    new = torch.randn(2, 123, 2, 64, device=DEV).to(torch.bfloat16)
+    cu = torch.tensor([0, 90, 90, 123], dtype=torch.int32, device=DEV)
+    c.append(new[0], new[1], ref.table, ref.lens, cu)
+    ref.k, ref.v, ref.ks, ref.vs = c.k, c.v, c.k_scale, c.v_scale
+    q = make_q(3, 4, 64)
+    o, L = c.decode(q, ref.table, ref.lens, 0.2)
+    k, v = c.gather(ref.table, ref.lens, 90, rep=2)
+    ok()
+    check_decode(o, L, decode_exact(ref, q, 0.2))
+    if not e4m3:
+        assert torch.equal(k[0, 2], new[0, :90, 1]) and torch.equal(v[2, 1, :33], new[1, 90:, 0])
+    assert (k[1] == 0).all() and (v[2, :, 33:] == 0).all()
+
+
+# --------------------------------------------------------------- guard bands
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_nothing_around_the_outputs_is_touched(e4m3):
+    """Outputs and workspace inside larger buffers; a cache with gaps between rows, heads and pages."""
+    B, H, Hq, d, page = 5, 3, 9, 64, 16
+    c = Cache([40, 0, 129, 16, 700], H, d, page, e4m3, "padded", seed=72)
+    q = make_q(B, Hq, d)
+    ob, lb = torch.full((B * Hq * d + 64,), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((B * Hq + 8,), 7.0, device=DEV)
+    size = fa.fa_decode_workspace_bytes(B, Hq, H, d)
+    wb = torch.full((size + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    o, L = ob[32:-32].view(B, Hq, d), lb[4:-4].view(B, Hq)
+    fa.fa_decode(q, c.k, c.v, o=o, lse=L, scale=0.125, workspace=wb[32:-32], **c.args)
+    ok()
+    check_decode(o, L, decode_exact(c, q, 0.125))
+    for buf, n in ((ob, 32), (lb, 4), (wb, 32)):
+        edge = buf[0]
+        assert (buf[:n] == edge).all() and (buf[-n:] == edge).all()
+    # append: every byte of the storage but the new rows (and their factors) stays.
+    bases = [x._base if x._base is not None else x for x in (c.k, c.v)]
+    before = [b.clone() for b in bases]
+    new = torch.randn(B, H, d, device=DEV).to(torch.bfloat16)
+    fa.fa_cache_append(new, new, c.k, c.v, **c.args)
+    ok()
+    for x, base, was in zip((c.k, c.v), bases, before):
+        now = base.clone()
+        page_ids, off = zip(*[c.where(b, torch.tensor([n - 1], device=DEV)) for b, n in enumerate(c.lens.tolist()) if n])
+        for pg, of in zip(page_ids, off):
+            now[pg[0], :H, of[0], :d] = was[pg[0], :H, of[0], :d]
+        assert same(now, was)
+    # gather
+    gb = torch.full((B * H * 2 * 50 * d + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = gb[32:-32].view(B, H * 2, 50, d)
+    fa.fa_cache_gather(c.k, c.v, k_out=out, v_out=None, **c.args)
+    ok()
+    assert (gb[:32] == 7).all() and (gb[-32:] == 7).all() and torch.isfinite(out.float()).all()
