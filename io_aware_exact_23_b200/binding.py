@@ -341,31 +341,34 @@ def fa_dropout_mask(B: int, H: int, N: int, rate: float, seed: int, offset: int,
 
 
 # ------------------------------------------------------------ key/value cache
+# A decode step calls these once a layer and little else happens on the host, so the checks
+# are written for the case that they hold: each tensor is looked at in line, and _check_on
+# says what is wrong with one that does not pass (or accepts a subclass of Tensor).
 CACHE_BF16, CACHE_E4M3 = 0, 1
 _STRIDES2 = struct.Struct("@2q")
+_Tensor, _BF16, _U8, _I32, _F32 = torch.Tensor, torch.bfloat16, torch.uint8, torch.int32, torch.float32
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _check_on(t, name: str, dtype, shape, device: int):
     """Type, device and shape of a tensor whose strides the caller deals with."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == device:
-        return
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda or t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
-    if t.shape != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale):
+def _paged_cache(k, v, block_table, seq_lens, k_scale, v_scale):
     """The packed C description of a cache held in torch tensors (any strides with adjacent
     row elements), and (device, B, H, d)."""
-    if not isinstance(k_cache, torch.Tensor) or not isinstance(block_table, torch.Tensor):
+    if not isinstance(k, _Tensor) or not isinstance(block_table, _Tensor):
         raise TypeError("k_cache and block_table must be torch.Tensor")
-    dt, dev, shape, table = k_cache.dtype, k_cache.get_device(), k_cache.shape, block_table.shape
-    if dt is not torch.bfloat16 and dt is not torch.uint8:
+    dt, dev, shape, table = k.dtype, k.get_device(), k.shape, block_table.shape
+    if dt is not _BF16 and dt is not _U8:
         raise TypeError(f"k_cache must be torch.bfloat16 or torch.uint8 (e4m3 codes), got {dt}")
     if dev < 0:
         raise ValueError("k_cache must be a CUDA tensor")
@@ -373,36 +376,42 @@ def _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale):
         raise ValueError("k_cache is [pages, H, page_size, d] and block_table [B, max_pages]")
     P, H, page, d = shape
     B, per = table
-    _check_on(v_cache, "v_cache", dt, shape, dev)
-    _check_on(block_table, "block_table", torch.int32, table, dev)
-    _check_on(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    k0, k1, k2, k3 = k_cache.stride()
-    v0, v1, v2, v3 = v_cache.stride()
+    if not (type(v) is _Tensor and v.dtype is dt and v.get_device() == dev and v.shape == shape):
+        _check_on(v, "v_cache", dt, shape, dev)
+    if not (block_table.dtype is _I32 and block_table.get_device() == dev):
+        _check_on(block_table, "block_table", _I32, table, dev)
+    if not (type(seq_lens) is _Tensor and seq_lens.dtype is _I32 and seq_lens.get_device() == dev and
+            seq_lens.shape == (B,)):
+        _check_on(seq_lens, "seq_lens", _I32, (B,), dev)
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
     b0, b1 = block_table.stride()
     if (d > 1 and (k3 != 1 or v3 != 1)) or (per > 1 and b1 != 1) or (B > 1 and seq_lens.stride(0) != 1):
         raise ValueError("the last dimension of k_cache, v_cache, block_table and seq_lens must be contiguous")
-    if dt is torch.bfloat16:
+    if dt is _BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale belong to a cache of e4m3 codes (torch.uint8)")
-        return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), 0, 0, k0, k1, k2, v0, v1, v2, 0, 0, 0, 0, 0, 0,
+        return _PAGED_CACHE.pack(k.data_ptr(), v.data_ptr(), 0, 0, k0, k1, k2, v0, v1, v2, 0, 0, 0, 0, 0, 0,
                                  block_table.data_ptr(), seq_lens.data_ptr(), b0, CACHE_BF16, P, H, page, d, B,
                                  per), dev, B, H, d
-    _check_on(k_scale, "k_scale", torch.float32, (P, H, page), dev)
-    _check_on(v_scale, "v_scale", torch.float32, (P, H, page), dev)
-    return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k0, k1, k2,
-                             v0, v1, v2, *k_scale.stride(), *v_scale.stride(), block_table.data_ptr(),
-                             seq_lens.data_ptr(), b0, CACHE_E4M3, P, H, page, d, B, per), dev, B, H, d
+    rows = (P, H, page)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if not (type(t) is _Tensor and t.dtype is _F32 and t.get_device() == dev and t.shape == rows):
+            _check_on(t, name, _F32, rows, dev)
+    return _PAGED_CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k0, k1, k2, v0, v1, v2,
+                             *k_scale.stride(), *v_scale.stride(), block_table.data_ptr(), seq_lens.data_ptr(), b0,
+                             CACHE_E4M3, P, H, page, d, B, per), dev, B, H, d
 
 
 def _call_on(device: int, where: str, stream, fn, *args) -> None:
     """Call a C entry point with ``device`` current, on ``stream`` (its current stream by default)."""
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device)
+        handle = _raw_stream(device)
     elif stream.device.index != device:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on cuda:{device}")
     else:
         handle = stream.cuda_stream
-    if torch._C._cuda_getDevice() == device:
+    if _current_device() == device:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -423,24 +432,27 @@ def fa_cache_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, cu_ne
     else int32 [B + 1], tokens ``cu_new[b]:cu_new[b+1]`` end sequence b.
     """
     c, dev, B, H, d = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
-    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
+    if not isinstance(k_new, _Tensor) or k_new.dim() != 3:
         raise ValueError("k_new must be a [T, H, d] tensor")
     T = k_new.shape[0]
-    _check_on(k_new, "k_new", torch.bfloat16, (T, H, d), dev)
-    _check_on(v_new, "v_new", torch.bfloat16, (T, H, d), dev)
-    ks, vs = k_new.stride(), v_new.stride()
-    if T and (ks[2] != 1 or vs[2] != 1):
+    rows = (T, H, d)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if not (type(t) is _Tensor and t.dtype is _BF16 and t.get_device() == dev and t.shape == rows):
+            _check_on(t, name, _BF16, rows, dev)
+    k0, k1, k2 = k_new.stride()
+    v0, v1, v2 = v_new.stride()
+    if T and (k2 != 1 or v2 != 1):
         raise ValueError("the last dimension of k_new and v_new must be contiguous")
     cu = None
     if cu_new is not None:
-        _check_on(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+        _check_on(cu_new, "cu_new", _I32, (B + 1,), dev)
         if not cu_new.is_contiguous():
             raise ValueError("cu_new must be contiguous")
         cu = cu_new.data_ptr()
     elif T != B:
         raise ValueError(f"k_new has {T} tokens for {B} sequences: pass cu_new")
     _call_on(dev, "fa_cache_append", stream, _lib.fa_cache_append, c, k_new.data_ptr(), v_new.data_ptr(),
-             _STRIDES2.pack(ks[0], ks[1]), _STRIDES2.pack(vs[0], vs[1]), T, cu)
+             _STRIDES2.pack(k0, k1), _STRIDES2.pack(v0, v1), T, cu)
 
 
 def fa_cache_gather(k_cache, v_cache, block_table, seq_lens, k_out, v_out, k_scale=None, v_scale=None,
@@ -453,16 +465,21 @@ def fa_cache_gather(k_cache, v_cache, block_table, seq_lens, k_out, v_out, k_sca
     """
     c, dev, B, H, d = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
     out = k_out if k_out is not None else v_out
-    if not isinstance(out, torch.Tensor) or out.dim() != 4 or out.shape[1] % H != 0:
+    if not isinstance(out, _Tensor) or out.dim() != 4 or out.shape[1] % H != 0:
         raise ValueError(f"k_out and v_out are [B, {H} * rep, N, d] tensors, and one of them is needed")
-    shape = (B, out.shape[1], out.shape[2], d)
-    for nm, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            _check_on(t, nm, torch.bfloat16, shape, dev)
-            if not t.is_contiguous():
-                raise ValueError(f"{nm} must be contiguous")
-    _call_on(dev, "fa_cache_gather", stream, _lib.fa_cache_gather, c, None if k_out is None else k_out.data_ptr(),
-             None if v_out is None else v_out.data_ptr(), shape[1] // H, shape[2])
+    _, heads, N, _ = out.shape
+    shape = (B, heads, N, d)
+    ptrs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            ptrs.append(None)
+            continue
+        if not (type(t) is _Tensor and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape):
+            _check_on(t, name, _BF16, shape, dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        ptrs.append(t.data_ptr())
+    _call_on(dev, "fa_cache_gather", stream, _lib.fa_cache_gather, c, ptrs[0], ptrs[1], heads // H, N)
 
 
 def fa_decode_workspace_bytes(B: int, Hq: int, H: int, d: int) -> int:
@@ -479,20 +496,26 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
     is as in ``fa_cache_append``, the new token's key and value already in it.
     """
     c, dev, B, _, d = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be a [B, Hq, d] tensor")
     Hq = q.shape[1]
-    _check_on(q, "q", torch.bfloat16, (B, Hq, d), dev)
-    _check_on(o, "o", torch.bfloat16, (B, Hq, d), dev)
+    shape = (B, Hq, d)
+    for name, t in (("q", q), ("o", o)):
+        if not (type(t) is _Tensor and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape):
+            _check_on(t, name, _BF16, shape, dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
     lse_ptr = None
     if lse is not None:
-        _check_on(lse, "lse", torch.float32, (B, Hq), dev)
+        if not (type(lse) is _Tensor and lse.dtype is _F32 and lse.get_device() == dev and lse.shape == (B, Hq)):
+            _check_on(lse, "lse", _F32, (B, Hq), dev)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
         lse_ptr = lse.data_ptr()
-    _check_on(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
-    if not (q.is_contiguous() and o.is_contiguous() and workspace.is_contiguous()):
-        raise ValueError("q, o and workspace must be contiguous")
+    if not (type(workspace) is _Tensor and workspace.dtype is _U8 and workspace.get_device() == dev):
+        _check_on(workspace, "workspace", _U8, None, dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     _call_on(dev, "fa_decode", stream, _lib.fa_decode, c, q.data_ptr(), o.data_ptr(), lse_ptr, Hq, scale, window,
              workspace.data_ptr(), workspace.numel())
 
