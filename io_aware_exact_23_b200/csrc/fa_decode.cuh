@@ -95,8 +95,11 @@ struct DecodeCfg {
   // The share of a CTA is dealt out by cost: kTileCost a tile, and kItemCost for what an item
   // costs besides (its Q, first maximum, sums and epilogue).  256 short e4m3 sequences x 16
   // heads, d = 64: 57.1 us without an item's cost, 55.2 with 2, 57.4 with 4, 59.7 with 8; long
-  // sequences do not tell them apart.
-  static constexpr int kTileCost = 4, kItemCost = 2;
+  // sequences do not tell them apart.  Below kItemTiles tiles a CTA only the tiles count: one
+  // tile more is what a CTA then takes longer than the others (one sequence of 777, 8 heads:
+  // 9.9 us with an item's cost, which gives some of the 56 CTAs two tiles and others none, 8.4
+  // without; at 3 tiles a CTA 15.2 against 16.1 us speak for it).
+  static constexpr int kTileCost = 4, kItemCost = 2, kItemTiles = 2;
   static constexpr int kSmemMax = kCtas == 2 ? 115712 : 232448;
 
   static constexpr int kPOff = 0;
@@ -300,7 +303,7 @@ __device__ __forceinline__ void reduce_columns(float (&v)[N], F f) {
 }
 
 // `total` units of cost dealt out to `nc` CTAs, the first of them one more where it does not
-// divide.  A unit x of an item that begins at x0 stands for its tile (x - x0 - kItemCost) /
+// divide.  A unit x of an item that begins at x0 stands for its tile (x - x0 - item's cost) /
 // kTileCost (the first one below), so a CTA's tiles are those between the tiles that its
 // first unit and the next CTA's stand for.
 struct DecodeSplit {
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   int *words = reinterpret_cast<int *>(bars + C::kFixedBars);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(words);
   volatile int *abort_flag = words + 1;
-  // The share: first sequence, head and tile, -; total cost, CTAs with a share, first block of
+  // The share: first sequence, head and tile, an item's cost; total cost, CTAs with a share, first block of
   // heads, "do nothing"; first sequence's length, cost before the first item, first and end tile.
   int *share = words + 2;
   uint64_t *bar_full = reinterpret_cast<uint64_t *>(words + 16);  // [kSlots]
@@ -544,15 +547,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       if (raw != len) record_cache_error(p.c.status, kKernelDecode, b, p.c.seq);
       return ((len + 127) >> 7) - (DecodeWalk::first_of(p, len) >> 7);
     };
-    auto cost_of = [&](int n) { return n > 0 ? (C::kItemCost + C::kTileCost * n) * items : 0; };
-    int tiles = 0, cost = 0;
+    int tiles = 0, live = 0;  // of these sequences: tiles, and items that have any
 #pragma unroll 1
     for (int b = b_lo; b < b_hi; ++b) {
       const int n = tiles_of(b);
       tiles += n * items;
-      cost += cost_of(n);
+      live += n > 0 ? items : 0;
     }
-    int it = tiles, ic = cost;
+    int it = tiles, ic = live;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int ut = __shfl_up_sync(0xffffffffu, it, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
@@ -561,22 +563,26 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         ic += uc;
       }
     }
-    int total_t = __shfl_sync(0xffffffffu, it, 31), total_c = __shfl_sync(0xffffffffu, ic, 31);
-    int before_t = it - tiles, before_c = ic - cost;
+    int total_t = __shfl_sync(0xffffffffu, it, 31), total_i = __shfl_sync(0xffffffffu, ic, 31);
+    int before_t = it - tiles, before_i = ic - live;
     if (!small) {
       int2 *sums = reinterpret_cast<int2 *>(smem);  // [kWarps], before anything else is there
       if (lane == 31) sums[warp] = make_int2(it, ic);
       __syncthreads();
       const int2 v = lane < C::kWarps ? sums[lane] : make_int2(0, 0);
       total_t = __reduce_add_sync(0xffffffffu, v.x);
-      total_c = __reduce_add_sync(0xffffffffu, v.y);
+      total_i = __reduce_add_sync(0xffffffffu, v.y);
       before_t += __reduce_add_sync(0xffffffffu, lane < warp ? v.x : 0);
-      before_c += __reduce_add_sync(0xffffffffu, lane < warp ? v.y : 0);
+      before_i += __reduce_add_sync(0xffffffffu, lane < warp ? v.y : 0);
     } else {
       __syncthreads();  // share[] is zero
     }
     const int nc = min(static_cast<int>(gridDim.x), total_t), c = static_cast<int>(blockIdx.x);
     if (c < nc) {
+      const int extra = total_t / C::kItemTiles >= nc ? C::kItemCost : 0;
+      const int total_c = C::kTileCost * total_t + extra * total_i;
+      const int before_c = C::kTileCost * before_t + extra * before_i, cost = C::kTileCost * tiles + extra * live;
+      auto cost_of = [&](int n) { return n > 0 ? (extra + C::kTileCost * n) * items : 0; };
       const DecodeSplit sp(total_c, nc);
       // The share's first unit, and the next share's (of a small batch: by warp 0 and warp 1).
 #pragma unroll 1
@@ -591,8 +597,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           t0 += n * items;
           n = tiles_of(++b);
         }
-        const int one = C::kItemCost + C::kTileCost * n, item = at / one;
-        const int off = max(at - item * one - C::kItemCost, 0) / C::kTileCost;
+        const int one = extra + C::kTileCost * n, item = at / one;
+        const int off = max(at - item * one - extra, 0) / C::kTileCost;
         share[10 + e] = t0 + item * n + off;
         if (e == 0) {
           share[0] = b;
@@ -601,6 +607,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           share[6] = p.nblk == 1 ? 0 : item % p.nblk;
           share[8] = min(b == b_lo ? len_lo : __ldg(p.c.seq_lens + b), p.c.cap);
           share[9] = x - at + item * one;
+          share[3] = extra;
           share[4] = total_c;
           share[5] = nc;
         }
@@ -1170,7 +1177,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       }
     }
     if (!p.by_item && f == 0) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    const int total = share[4], nc = share[5], c = static_cast<int>(blockIdx.x);
+    const int extra = share[3], total = share[4], nc = share[5], c = static_cast<int>(blockIdx.x);
     int x0 = share[9];  // cost before the walk's item
     bool ok = true;
     for (int seg = 0; wk.rem > 0 && ok; ++seg) {
@@ -1225,7 +1232,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_o_empty[ob]);
-      const int cost = C::kItemCost + C::kTileCost * wk.n;
+      const int cost = extra + C::kTileCost * wk.n;
       if (starts && f == 0 && (p.by_item || !ends))
         decode_note(p, wk.b, wk.h, wk.blk, wk.h * p.G + g0, ends ? 0 : x0 + cost - 1, total, nc);
       if (ends) x0 += cost;
