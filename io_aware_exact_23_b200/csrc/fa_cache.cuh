@@ -1,8 +1,8 @@
 // fa_cache.cuh -- the paged key/value cache: its device view, the kernel that
 // writes new tokens into it and the kernel that reads sequences back.
 //
-// Both kernels move rows of d elements, one 16-byte chunk of 8 bf16 values per
-// thread, and do next to no arithmetic: their floor is the bytes they move at the
+// Both kernels move rows of d elements, in 16-byte chunks of 8 bf16 values
+// a thread, and do next to no arithmetic: their floor is the bytes they move at the
 // memory's rate.
 #pragma once
 
@@ -101,7 +101,7 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
 // Both kernels below give a warp `rows` (at most 32) rows of d elements.  Lane i first finds
 // where row i lies (sequence, page, strides: some hundred cycles of dependent loads and 64-bit
 // arithmetic, once per row), then the warp walks over the rows, kLanes lanes to a row with 16
-// bytes of bf16 each, taking the addresses from the lanes that know them.  (With every lane
+// bytes of bf16 (append: twice 16) each, taking the addresses from the lanes that know them.  (With every lane
 // finding its own piece's address, 145 to 245 instructions went into a piece, and the two
 // cases given below took 25 and 90 us.)
 constexpr int kCacheThreads = 256;
@@ -139,13 +139,15 @@ __device__ __forceinline__ uint64_t divide2(uint64_t x, uint64_t f, uint64_t r) 
 }
 
 // Rows are (token, K or V, head), head fastest.  Bound by its instructions: 8275 tokens x 8
-// heads x 128 as e4m3 take 15.0 us, 51 MB at 3.4 TB/s (five or six resident blocks, with fewer
-// registers: 17.1 us).
+// heads x 128 as e4m3 take 13.0 us, 51 MB at 3.9 TB/s, and 60000 tokens 67.9 us, 5.5 TB/s (with
+// one piece a lane, twice the lanes to a row and so twice the shuffles: 15.0 and 78.6 us; five
+// resident blocks, with fewer registers: 15.2 us; the next pass's loads ahead of this one's
+// division: 14.8 us, for want of registers).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kCacheThreads, 4) fa_cache_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kLanes = D / 8;         // lanes per row
+  constexpr int kLanes = D / 16;        // lanes per row, two 16-byte pieces each
   constexpr int kAtOnce = 32 / kLanes;  // rows per pass
-  constexpr int kBatch = 4;             // passes in flight
+  constexpr int kBatch = 2;             // passes in flight
   pdl_launch();
   pdl_wait();
   const CacheView &c = p.c;
@@ -186,10 +188,10 @@ __global__ void __launch_bounds__(kCacheThreads, 4) fa_cache_append_kernel(const
                                  row * c.scale_stride[which][2]);
     }
   }
-  const int chunk = lane % kLanes, sub = lane / kLanes;
+  const int chunk = lane % kLanes, sub = lane / kLanes;  // and chunk + kLanes
   float mine = 0.f;  // lane i: row i's factor
   for (int q0 = 0; q0 < rows; q0 += kBatch * kAtOnce) {
-    uint4 w[kBatch];
+    uint4 w[kBatch][2];
     uint8_t *to[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -197,21 +199,29 @@ __global__ void __launch_bounds__(kCacheThreads, 4) fa_cache_append_kernel(const
       const uint16_t *from = shfl_ptr(src, q & 31);
       to[k] = shfl_ptr(dst, q & 31);
       if (q >= rows) to[k] = nullptr;
-      w[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (to[k]) w[k] = __ldg(reinterpret_cast<const uint4 *>(from) + chunk);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[k][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (to[k]) w[k][i] = __ldg(reinterpret_cast<const uint4 *>(from) + chunk + i * kLanes);
+      }
     }
     if constexpr (!E4M3) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (to[k]) reinterpret_cast<uint4 *>(to[k])[chunk] = w[k];
+        if (to[k])
+#pragma unroll
+          for (int i = 0; i < 2; ++i) reinterpret_cast<uint4 *>(to[k])[chunk + i * kLanes] = w[k][i];
     } else {
       // The rows' largest magnitudes, as bf16 bits (a NaN is above all), brought to the rows'
       // lanes: lane q - q0 makes the factor of row q and its reciprocal, once for the row.
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        uint32_t m2 = __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu),
-                               __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu));
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[k][i].x & 0x7fff7fffu, w[k][i].y & 0x7fff7fffu),
+                                     __vmaxu2(w[k][i].z & 0x7fff7fffu, w[k][i].w & 0x7fff7fffu)));
         m2 = max(m2 >> 16, m2 & 0xffffu);
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) m2 = max(m2, __shfl_xor_sync(0xffffffffu, m2, o));
@@ -226,21 +236,24 @@ __global__ void __launch_bounds__(kCacheThreads, 4) fa_cache_append_kernel(const
       for (int k = 0; k < kBatch; ++k) {
         const float fk = __shfl_sync(0xffffffffu, f, k * kAtOnce + sub), rk = __shfl_sync(0xffffffffu, r, k * kAtOnce + sub);
         const uint64_t f2 = f2pack(fk, fk), r2 = f2pack(rk, rk);
-        const uint32_t words[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-        float a[8];
-        if (rk != 0.f) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) f2unpack(divide2(f2pack(bf16_lo(words[e]), bf16_hi(words[e])), f2, r2), a[2 * e], a[2 * e + 1]);
-        } else {
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t words[4] = {w[k][i].x, w[k][i].y, w[k][i].z, w[k][i].w};
+          float a[8];
+          if (rk != 0.f) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[2 * e] = __fdiv_rn(bf16_lo(words[e]), fk);
-            a[2 * e + 1] = __fdiv_rn(bf16_hi(words[e]), fk);
+            for (int e = 0; e < 4; ++e) f2unpack(divide2(f2pack(bf16_lo(words[e]), bf16_hi(words[e])), f2, r2), a[2 * e], a[2 * e + 1]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[2 * e] = __fdiv_rn(bf16_lo(words[e]), fk);
+              a[2 * e + 1] = __fdiv_rn(bf16_hi(words[e]), fk);
+            }
           }
+          if (to[k])
+            reinterpret_cast<uint2 *>(to[k])[chunk + i * kLanes] =
+                make_uint2(pack_e4m3x4(a[0], a[1], a[2], a[3]), pack_e4m3x4(a[4], a[5], a[6], a[7]));
         }
-        if (to[k])
-          reinterpret_cast<uint2 *>(to[k])[chunk] =
-              make_uint2(pack_e4m3x4(a[0], a[1], a[2], a[3]), pack_e4m3x4(a[4], a[5], a[6], a[7]));
       }
     }
   }

@@ -98,13 +98,14 @@ cudaError_t launch_early(void (*kernel)(Formal...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Rows of a warp of the append and gather kernels, in passes of 256 / d: eight passes, so that
-// most lanes find a row's address, but four (one round of loads) where eight would leave fewer
-// than 16 warps per SM.  8275 tokens x 8 heads x 128 written as e4m3 with eight / four passes:
-// 16.6 / 18.6 us; 300 positions x 8 heads x 128 read back four times: 3.9 / 3.6 us.
-int rows_per_warp(long long rows, int d, int num_sms) {
-  const int pass = 256 / d;
-  return rows >= 8ll * pass * 16 * num_sms ? 8 * pass : 4 * pass;
+// Rows of a warp of the append and gather kernels: `many`, so that most lanes find a row's
+// address, but one round of loads (1024 / d) where `many` would leave fewer than 16 warps per SM.
+// `many` is two rounds (300 positions x 8 heads x 128 read back four times, two rounds / one:
+// 3.9 / 3.6 us), and a whole warp's rows for appending e4m3, whose rows need most instructions:
+// 6000, 8275, 12000, 24000 and 60000 tokens x 8 heads x 128 with 16 / 32 rows take 10.9 / 11.8,
+// 14.1 / 13.0, 17.7 / 18.1, 31.8 / 30.4 and 72.6 / 67.9 us (bf16: 33.1 / 34.2 us at 24000).
+int rows_per_warp(long long rows, int d, int many, int num_sms) {
+  return rows >= 16ll * many * num_sms ? many : 1024 / d;
 }
 
 unsigned blocks_for(long long rows, int per_warp) {
@@ -211,10 +212,10 @@ int fa_cache_append(const fa_paged_cache *cache, const void *k_new, const void *
   p.T = T;
   const long long total = 2ll * T * cache->H;
   if (total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  p.rows = rows_per_warp(total, cache->d, ds->num_sms);
+  const bool e4m3 = cache->type == FA_CACHE_E4M3;
+  p.rows = rows_per_warp(total, cache->d, e4m3 ? 32 : 2048 / cache->d, ds->num_sms);
   const unsigned grid = blocks_for(total, p.rows);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool e4m3 = cache->type == FA_CACHE_E4M3;
   const auto kernel = cache->d == 64 ? (e4m3 ? fa::fa_cache_append_kernel<64, true> : fa::fa_cache_append_kernel<64, false>)
                                      : (e4m3 ? fa::fa_cache_append_kernel<128, true> : fa::fa_cache_append_kernel<128, false>);
   const cudaError_t e = launch_early(kernel, dim3(grid), fa::kCacheThreads, 0, s, p);
@@ -238,7 +239,7 @@ int fa_cache_gather(const fa_paged_cache *cache, void *k_out, void *v_out, int r
   p.rep = rep;
   p.N = N;
   const long long heads = static_cast<long long>(cache->B) * cache->H;
-  p.rows = rows_per_warp(heads * N, cache->d, ds->num_sms);
+  p.rows = rows_per_warp(heads * N, cache->d, 2048 / cache->d, ds->num_sms);
   p.parts = (N - 1) / p.rows + 1;
   const dim3 grid(blocks_for(heads * p.parts, 1), 2);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
