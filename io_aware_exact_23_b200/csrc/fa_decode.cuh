@@ -489,7 +489,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const WaitCtx ctx{p.c.status, abort_flag, kKernelDecode, p.c.seq};
-  pdl_launch();
   if (warp == C::kQWarp) {
     if (lane < 2) {
       mbar_init(&bar_q[lane], 32);
@@ -528,6 +527,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   if (warp == C::kIssuer) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
+    // Only now: a kernel that starts early must not take the tensor memory that this one, which
+    // it will wait for, has yet to get.
+    pdl_launch();
   }
   pdl_wait();  // nothing before this reads or writes what the stream's earlier kernels may touch
 

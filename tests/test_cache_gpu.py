@@ -732,3 +732,78 @@ def test_nothing_around_the_outputs_is_touched(e4m3):
     fa.fa_cache_gather(c.k, c.v, k_out=out, v_out=None, **c.args)
     ok()
     assert (gb[:32] == 7).all() and (gb[-32:] == 7).all() and torch.isfinite(out.float()).all()
+
+
+# ------------------------------------- kernels that begin while the last one ends
+def test_decodes_of_every_kind_in_a_row():
+    """Decode calls of all instances, with one workspace and no wait in between, on one
+    stream and on two at once, return the bits that they return one at a time."""
+    kinds = [(G, d, e) for G in (1, 3, 8, 16, 32) for d in (64, 128) for e in (False, True)]
+    work = []
+    for i, (G, d, e) in enumerate(kinds):
+        c = Cache([1 + 37 * i, 0, 300 - 7 * i], 2, d, 16, e, seed=80 + i)
+        q = make_q(3, 2 * G, d, seed=i)
+        alone = decode(c, q)
+        torch.cuda.synchronize()
+        work.append((c, q, alone))
+    size = max(fa.fa_decode_workspace_bytes(3, q.shape[1], 2, q.shape[2]) for _, q, _ in work)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    for used in ((0,), (0, 1)):
+        got = []
+        for r in range(4):
+            for i in range(len(work)):
+                for j in used:
+                    c, q, alone = work[i if j == 0 else len(work) - 1 - i]
+                    with torch.cuda.stream(streams[j]):
+                        got.append((decode(c, q, ws=spaces[j]), alone))
+        torch.cuda.synchronize()
+        ok()
+        for (o, L), (o1, L1) in got:
+            assert torch.equal(o, o1) and torch.equal(L, L1)
+
+
+def test_graph_whose_branches_meet():
+    """A graph where an append waits for two branches and two decodes for it."""
+    H, d = 2, 128
+    n = [129, 4, 700]
+    c = Cache(n, H, d, 16, True, seed=91)
+    for b in range(3):  # the last position is the graph's to write
+        c.put(c.k, c.ks, b, torch.tensor([n[b] - 1], device=DEV), torch.zeros(1, H, d, device=DEV))
+    x = torch.zeros(2, 3, H, d, dtype=torch.bfloat16, device=DEV)
+    src = torch.randn(2, 3, H, d, device=DEV).to(torch.bfloat16)
+    q = [make_q(3, 8, d, seed=s) for s in (5, 6)]
+    ws = [torch.empty(fa.fa_decode_workspace_bytes(3, 8, H, d), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    res = [decode(c, q[i], ws=ws[i]) for i in range(2)]
+    old = decode_exact(c, q[1], 1 / math.sqrt(d))
+    check_decode(*res[1], old)
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x[1].copy_(src[1])
+            decode(c, q[1], ws=ws[1], out=res[1][0])  # the old contents: to be over before the append
+        x[0].copy_(src[0])
+        main.wait_stream(side)
+        fa.fa_cache_append(x[0], x[1], c.k, c.v, **c.args)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            second = decode(c, q[1], ws=ws[1])
+        first = decode(c, q[0], ws=ws[0])
+        main.wait_stream(side)
+    g.replay()
+    torch.cuda.synchronize()
+    ok()
+    check_decode(res[1][0], res[1][1], old)
+    for b in range(3):
+        for which, rows, f in (("k", c.k, c.ks), ("v", c.v, c.vs)):
+            want = src[0 if which == "k" else 1][b].double()
+            got = c.rows(which, b, n[b])[:, -1]
+            top = want.abs().amax(-1, keepdim=True)
+            # half a step of e4m3: 2^-4 of the value, or 2^-10 code units below its normal numbers
+            assert ((got - want).abs() <= want.abs() * 2.0**-4 + top / 448 * 2.0**-10 * (1 + 2.0**-20)).all()
+    for got, qq in ((first, q[0]), (second, q[1])):
+        check_decode(*got, decode_exact(c, qq, 1 / math.sqrt(d)))
