@@ -10,6 +10,12 @@
 // tensor core, and no thread ever holds an element of them.  A thread's work is one
 // key's G scores.
 //
+// Measured, in a replayed graph, of the 6465 GB/s that a copy reaches here: 1 x 131072 x 16
+// heads of d = 128 in bf16 161 us (1074 MB, 6.65 TB/s: reads alone), 64 ragged sequences of up to
+// 8192 x 8 heads in e4m3 94 us (551 MB, 5.9 TB/s; SMs differ by 6% in their time per tile).  Where
+// a CTA has few tiles the time is latency: one sequence of 777 takes 8.4 us, 3 to the first load
+// (lengths, share, page ids), 3 for a tile, 2.4 for the join.
+//
 // Work split.  A tile is 128 positions of one (sequence, cache head, block of at most GB
 // query heads).  All tiles, in that order, are dealt out evenly: CTA c of nc takes tiles
 // [T c / nc, T (c + 1) / nc), so SMs finish together whatever the lengths, and a sequence
