@@ -117,8 +117,9 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int H, int d);
  * over positions j in [max(0, len - window), len) of cache head h / (Hq / H), with
  * len = seq_lens[b] (the new token's own key and value already appended); window = 0
  * means all of them.  q, o: [B, Hq, d] bf16, contiguous; lse: [B, Hq] fp32 (natural
- * log) or NULL.  Hq is a multiple of H.  A sequence of length 0 gets o = 0 and
- * lse = -inf.  Scores, statistics and sums are fp32; o is rounded once, to bf16.
+ * log) or NULL.  Hq is a multiple of H.  o may be q itself (a row of q is last read
+ * before its row of o is written), and overlaps nothing else.  A sequence of length 0
+ * gets o = 0 and lse = -inf.  Scores, statistics and sums are fp32; o is rounded once, to bf16.
  * The result does not depend on where the pages lie, and repeated calls on the
  * same GPU return the same bits.
  */

@@ -492,8 +492,9 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
 
     ``q``, ``o``: bf16 [B, Hq, d], Hq a multiple of the cache's heads; ``lse``: fp32
     [B, Hq] or None; ``workspace``: uint8, ``fa_decode_workspace_bytes`` long;
-    ``window``: how many of a sequence's last positions are seen (0: all).  The cache
-    is as in ``fa_cache_append``, the new token's key and value already in it.
+    ``window``: how many of a sequence's last positions are seen (0: all).  ``o`` may be
+    ``q`` itself.  The cache is as in ``fa_cache_append``, the new token's key and value
+    already in it.
     """
     c, dev, B, _, d = _paged_cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
     if not isinstance(q, _Tensor) or q.dim() != 3:
@@ -516,6 +517,8 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
         _check_on(workspace, "workspace", _U8, None, dev)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    if not 0 <= window <= 0x7FFFFFFF:  # ctypes would keep the low 32 bits: more than any length, or refused
+        window = 0 if window > 0 else -1
     _call_on(dev, "fa_decode", stream, _lib.fa_decode, c, q.data_ptr(), o.data_ptr(), lse_ptr, Hq, scale, window,
              workspace.data_ptr(), workspace.numel())
 

@@ -807,3 +807,31 @@ def test_graph_whose_branches_meet():
             assert ((got - want).abs() <= want.abs() * 2.0**-4 + top / 448 * 2.0**-10 * (1 + 2.0**-20)).all()
     for got, qq in ((first, q[0]), (second, q[1])):
         check_decode(*got, decode_exact(c, qq, 1 / math.sqrt(d)))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("lens", [[5000], [0, 3, 129, 0, 64, 1000], [100] * 200])
+def test_decode_in_place(lens, e4m3):
+    """o = q: sequences held by one CTA, split ones and idle ones."""
+    c = Cache(lens, 2, 64, 32, e4m3, seed=95)
+    for G in (2, 40):
+        q = make_q(len(lens), 2 * G, 64, seed=G)
+        o, L = run_decode(c, q)
+        same = q.clone()
+        _, L2 = decode(c, same, out=same)
+        ok()
+        assert torch.equal(same, o) and torch.equal(L2, L)
+
+
+def test_decode_window_beyond_31_bits():
+    c = Cache([300, 17], 1, 64, 16, False, seed=96)
+    q = make_q(2, 4, 64)
+    o, L = run_decode(c, q)
+    for window in (2**31 - 1, 2**31, 2**32 + 5):
+        o2, L2 = decode(c, q, window=window)
+        ok()
+        assert torch.equal(o, o2) and torch.equal(L, L2)
+    for window in (-1, -(2**31), 5 - 2**32):
+        with pytest.raises(fa.FaError) as e:
+            decode(c, q, window=window)
+        assert e.value.code == 1
