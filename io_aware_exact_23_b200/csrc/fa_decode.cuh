@@ -1087,7 +1087,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             part[1][g] = pack_bf16(a - bf16_lo(part[0][g]), b - bf16_hi(part[0][g]));
           } else {
             const float fw = fv * vinv;
-            uint32_t r = pack_f16(a * fw, b * fw);
+            float wa, wb;
+            f2unpack(mul2(f2pack(a, b), f2pack(fw, fw)), wa, wb);
+            uint32_t r = pack_f16(wa, wb);
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
               const uint16_t c = f16x2_to_e4m3x2(r);
