@@ -33,7 +33,8 @@
  * outside [0, max_pages * page_size] that a call meets is never followed: the
  * call records FA_ERR_DEVICE_CACHE (read it with fa_device_status; the info words
  * are kernel id (6 append, 7 gather, 8 decode), sequence, block, launch number),
- * and that sequence's outputs are undefined while the others' hold.
+ * and that sequence's outputs are undefined while the others' hold.  A timeout
+ * or another failure of any kernel goes before it: it is what the status says then.
  *
  * Calls follow fa.h: asynchronous on `stream`, argument errors returned before
  * anything is launched, no allocation beyond the library's status block, nothing

@@ -537,18 +537,19 @@ int fa_device_status_info(void *stream, int *info) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
-  if (h[0] == 0) return FA_OK;
+  const bool cache = h[0] == 0;  // at most a page id or a length out of range (record_cache_error)
+  if (cache && h[5] == 0) return FA_OK;
   if (info) {
-    info[0] = h[1];
-    info[1] = h[2];
-    info[2] = h[3];
-    info[3] = h[0] == FA_ERR_DEVICE_CACHE ? h[5] : h[4];
+    info[0] = cache ? h[7] & 15 : h[1];
+    info[1] = cache ? h[6] : h[2];
+    info[2] = cache ? h[7] >> 4 : h[3];
+    info[3] = cache ? h[5] : h[4];
   }
   if (cudaMemset(ds->status, 0, kStatusInts * sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_CUDA;
   }
-  if (h[0] == FA_ERR_DEVICE_CACHE) return FA_ERR_DEVICE_CACHE;
+  if (cache) return FA_ERR_DEVICE_CACHE;
   return h[0] == fa::kStatusInternal ? FA_ERR_DEVICE_INTERNAL : FA_ERR_DEVICE_TIMEOUT;
 }
 

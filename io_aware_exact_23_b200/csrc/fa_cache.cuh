@@ -15,7 +15,6 @@
 
 namespace fa {
 
-enum : int { kStatusCache = 9 };
 enum : int { kKernelAppend = 6, kKernelGather = 7, kKernelDecode = 8 };
 
 // Programmatic dependent launch.  The cache's kernels are launched so that they may start while
@@ -41,15 +40,14 @@ struct CacheView {
   int seq;
 };
 
-// Record a page id or a length out of range (the first one sticks).  Word 4 of the
-// status block stays as it is: it makes a pipeline of that launch give up, and
-// these kernels carry on with their other sequences.
+// Record a page id or a length out of range (the first one sticks): words 5 to 7 of the status
+// block, launch number, sequence, and block and kernel.  Words 0 to 4 are those of failures that
+// spoil more than a sequence (ptx.cuh), which must not be hidden by this one; word 4 also makes
+// a pipeline of that launch give up, and these kernels carry on with their other sequences.
 __device__ __noinline__ void record_cache_error(int *status, int kernel, int b, int seq) {
-  if (atomicCAS(status, 0, kStatusCache) == 0) {
-    status[1] = kernel;
-    status[2] = b;
-    status[3] = static_cast<int>(blockIdx.x);
-    status[5] = seq;
+  if (atomicCAS(status + 5, 0, seq) == 0) {
+    status[6] = b;
+    status[7] = static_cast<int>(blockIdx.x) << 4 | kernel;
   }
 }
 
