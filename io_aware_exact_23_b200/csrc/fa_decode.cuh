@@ -1270,10 +1270,10 @@ __host__ __device__ inline bool decode_entry_ok(int b, int row, int parts, int c
 }
 
 // Joins the parts of the item of entry blockIdx.x for query head blockIdx.y of its block: it
-// starts in CTA c (its second slot) and goes on in the first slots of CTAs c + 1 ...  A part of weight 0
-// may be empty and is not read into the sum.  The order of every sum is fixed by the number
-// of parts.  Two dependent loads deep (which item, then its parts) and one barrier: the
-// kernel's time is its latency.
+// starts in CTA c (its second slot) and goes on in the first slots of CTAs c + 1 ...  An empty part
+// (m = -inf, O as the workspace held it) is not read into the sum; a part of weight 0 is, so that
+// a NaN in it stays one.  The order of every sum is fixed by the number of parts.  Two dependent
+// loads deep (which item, then its parts) and one barrier: the kernel's time is its latency.
 constexpr int kJoinThreads = 256;
 
 template <int D, int GB>
@@ -1310,7 +1310,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __gr
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = grp; i < mt.z; i += kGroups) {
     const float w = ex2(mine.x - M);
-    if (w != 0.f) {
+    if (mine.x != -INFINITY) {
       acc.x += w * o.x;
       acc.y += w * o.y;
       acc.z += w * o.z;
