@@ -326,20 +326,20 @@ __global__ void __launch_bounds__(kCacheThreads, E4M3 ? 7 : 6) fa_cache_gather_k
     for (int k = 0; k < kBatch; ++k) {
       const int q = q0 + k * kAtOnce + sub;
       if constexpr (E4M3) {
+        // Rows behind a sequence's end are code 0 times factor 0; of any other row every code counts,
+        // zeros too: the factor may be an infinity or NaN, and a zero has a sign.
         const float s = __shfl_sync(0xffffffffu, f, q & 31);
-        if ((w[k].x | w[k].y) != 0) {  // rows behind a sequence's end are zeros already
-          const uint64_t s2 = f2pack(s, s);
-          const uint32_t codes[2] = {w[k].x, w[k].y};
-          uint32_t r[4];
+        const uint64_t s2 = f2pack(s, s);
+        const uint32_t codes[2] = {w[k].x, w[k].y};
+        uint32_t r[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(codes[e >> 1] >> (16 * (e & 1))));
-            float x, y;
-            f2unpack(mul2(f2pack(a.x, a.y), s2), x, y);
-            r[e] = pack_bf16(x, y);
-          }
-          w[k] = make_uint4(r[0], r[1], r[2], r[3]);
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(codes[e >> 1] >> (16 * (e & 1))));
+          float x, y;
+          f2unpack(mul2(f2pack(a.x, a.y), s2), x, y);
+          r[e] = pack_bf16(x, y);
         }
+        w[k] = make_uint4(r[0], r[1], r[2], r[3]);
       }
       if (q < rows) {
         uint16_t *at = out + q * D + chunk * 8;

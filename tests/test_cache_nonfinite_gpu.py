@@ -19,6 +19,38 @@ def queries(B, Hq, d, seed=0):
     return torch.randn(B, Hq, d, generator=g).to(torch.bfloat16).to(DEV)
 
 
+# ------------------------------------------------------------------ gather
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_gather_of_a_quantised_row_that_was_not_finite(value, d):
+    """Such a row is NaN throughout, and the rows around it are what they were."""
+    n = 40
+    c = Cache([n], 2, d, 16, True, seed=1)
+    x = torch.randn(1, 2, d, device=DEV).abs().to(torch.bfloat16)  # codes of +0 under an infinite factor
+    x[0, 1, 17] = value
+    fa.fa_cache_append(x, x, c.k, c.v, **c.args)  # position n - 1
+    k, v = (torch.zeros(1, 4, n + 3, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    fa.fa_cache_gather(c.k, c.v, k_out=k, v_out=v, **c.args)
+    assert fa.fa_device_status() == 0
+    for t in (k, v):
+        assert torch.isnan(t[0, 2:, n - 1]).all()
+        assert torch.isfinite(t[0, :2]).all() and torch.isfinite(t[0, 2:, :n - 1]).all() and (t[0, :, n:] == 0).all()
+
+
+def test_gather_multiplies_every_code():
+    """Zero codes under factors that are not finite; zero codes with a sign."""
+    c = Cache([4], 1, 64, 16, True, seed=2)
+    page, off = c.where(0, torch.arange(4, device=DEV))
+    c.k[page, :, off] = 0
+    c.k[page[3], 0, off[3]] = 0x80
+    c.ks[page[0], 0, off[0]], c.ks[page[1], 0, off[1]] = math.inf, math.nan
+    out = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    fa.fa_cache_gather(c.k, c.v, k_out=out, v_out=None, **c.args)
+    assert fa.fa_device_status() == 0
+    assert torch.isnan(out[0, 0, :2]).all() and (out[0, 0, 2:] == 0).all()
+    assert torch.signbit(out[0, 0, 3]).all() and not torch.signbit(out[0, 0, 2]).any()
+
+
 # ------------------------------------------------------------ parts of a sequence
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("B", [1, 400])
