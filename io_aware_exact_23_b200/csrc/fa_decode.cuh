@@ -1228,7 +1228,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           float v = __uint_as_float(o[0][e]);
           if constexpr (E4M3)
             v += (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.0625f) * 0.0625f;
-          else
+          else if (fabsf(v) != INFINITY)  // an infinite value: the low part's product with it may be NaN
             v += __uint_as_float(o[1][e]);
           v *= __shfl_sync(0xffffffffu, mul, e);
           if (gc + e < ng) {

@@ -70,3 +70,18 @@ def test_a_nan_value_of_next_to_no_weight(B, e4m3):
     assert torch.isnan(o[:, :, 5]).all()
     o[:, :, 5] = 0
     assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("G", [1, 4, 8, 32])
+@pytest.mark.parametrize("n", [50, 9000])
+def test_an_infinite_value_in_bf16(n, G):
+    """One infinity is an infinity of its sign in that feature, two of different signs are NaN."""
+    for d in (64, 128):
+        c = Cache([n, n], 1, d, 16, False, seed=7)
+        for b, p, f, x in ((0, 7, 2, math.inf), (0, 30, 3, -math.inf), (0, 8, 4, math.inf), (0, 41, 4, -math.inf)):
+            page, off = c.where(b, torch.tensor([p], device=DEV))
+            c.v[page[0], 0, off[0], f] = x
+        q = queries(2, G, d)
+        o, L = run(fa, c, q, scale=0.1)
+        assert (o[0, :, 2] == math.inf).all() and (o[0, :, 3] == -math.inf).all() and torch.isnan(o[0, :, 4]).all()
+        assert torch.isfinite(o[0, :, 5:]).all() and torch.isfinite(o[1]).all() and torch.isfinite(L).all()
