@@ -65,8 +65,8 @@ def test_no_entry_leads_out_of_the_buffers(tmp_path):
 
 
 def test_the_join_kernel_checks_before_it_follows():
-    """The check stands between the entry's load and its first use, beside the status of the launch."""
+    """The check stands between the entry's load and its first use."""
     src = open(os.path.join(CSRC, "fa_decode.cuh")).read()
     body = src[src.index("fa_decode_join_kernel(const"):]
     load, check, use = body.index("p.meta[blockIdx.x]"), body.index("decode_entry_ok("), body.index("auto row")
-    assert load < check < use and body.index("failed == p.c.seq") < use
+    assert load < check < use
