@@ -29,8 +29,10 @@
 // * bf16: P = hi + lo, both bf16 (16 significant bits), as 2 GB columns of O^T;
 // * e4m3: codes are multiplied as they are (kind::f8f6f4), the factor of K goes into the
 //   score, that of V into the weight.  q (8 bits, scaled by one power of two per 8 heads) is
-//   hi + lo / 16 in e4m3, exact to 2^-20 of its largest element; weights, taken to fp16,
-//   are hi + mid / 16 + lo / 256: 11 bits, and not less than 2^-20 of the largest weight.
+//   hi + lo / 16 in e4m3, exact to 2^-20 of its largest element.  A weight times V's factor is
+//   four e5m2 parts (decode_parts): off by 2^-15 of itself at most, or by 2^-32 of the head's
+//   largest such product, so that many keys far below one still count (three e4m3 parts of
+//   fp16's 11 bits stopped at 2^-20 of it).
 // The columns' sums meet again in fp32.
 //
 // Softmax warps.  Four warps own the 128 keys of a tile for 8 query heads, GB / 8 such
@@ -81,17 +83,19 @@ struct DecodeCfg {
   static constexpr int kQUsed = E4M3 ? 2 * GB : GB;                // rows of Q that are written
   static constexpr int kQRows = kQUsed < 8 ? 8 : kQUsed;           // rows of Q in shared memory
   static constexpr int kQCols = kQRows < 16 ? 16 : kQRows;         // columns of S^T
-  static constexpr int kOParts = E4M3 ? 3 : 2;
+  static constexpr int kOParts = E4M3 ? 4 : 2;
   static constexpr int kOCols = (kOParts * GB + 15) / 16 * 16;     // columns of O^T
   static constexpr int kPRow = GB <= 8 ? 32 : 4 * GB;              // bytes of a key's row of P
   static constexpr int kQBytes = kQRows * kRowBytes;
   static constexpr int kPBytes = 128 * kPRow;
   static constexpr int kScStages = 4;  // ring of the keys' factors (e4m3)
-  // A score may exceed the running reference by kGrow (log2) before the reference moves;
-  // e4m3 weights leave room for it below 448.
-  // (With 2^3 instead of 2^5 in e4m3, the first tiles of most segments moved it.)
-  static constexpr float kGrow = E4M3 ? 5.f : 8.f;
-  static constexpr int kWeightLog2 = 3;  // e4m3: a weight of 1 is code value 8, 2^kGrow is 256
+  // A score may exceed the running reference by kGrow (log2) before the reference moves.  e4m3: what
+  // goes into the product is a code, weight * V's factor * a power of two per 8 heads.  A head's
+  // reference is put so that its largest code is 2^kCodeLog2 (decode_references), and moves before a
+  // code passes 2^(kCodeLog2 + kGrowV), or a weight 2^(kHeadLog2 + kGrow).
+  // (Room of 2^3 for the codes' growth instead of 2^5: the first tiles of most segments moved it.)
+  static constexpr float kGrow = 8.f;
+  static constexpr int kCodeLog2 = 4, kGrowV = 5, kHeadLog2 = 60;
 
   static constexpr int kSoftmaxWarps = 4 * kGroups;
   static constexpr int kWarps = kSoftmaxWarps + 8;  // softmax, 4 epilogue, producer, issuer, Q, scales
@@ -111,10 +115,10 @@ struct DecodeCfg {
   static constexpr int kPOff = 0;
   static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kRingOff = (kQOff + 2 * kQBytes + 1023) / 1024 * 1024;
-  // Behind the ring: factors, then floats xmax[2][GB][4], lpart[2][4][GB], mstat[2][GB],
-  // vmax[kGroups][2][4], qscale[2][kGroups], vstat[2][kGroups], then barriers and words.
+  // Behind the ring: factors, then floats xmax[2][GB][4], lpart[2][4][GB], mstat[2][GB], of e4m3
+  // vmax[2][GB][4] and refs[4][3][GB], and qscale[2][kGroups], vstat[2][kGroups], then barriers and words.
   static constexpr int kScBytes = E4M3 ? kScStages * 1024 : 0;
-  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + 2 * kGroups + 8 * kGroups + 2 * kGroups;
+  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + (E4M3 ? 20 * GB : 0) + 4 * kGroups;
   static constexpr int kFixedBars = 20 + 2 * kScStages;
   static constexpr int kTailBytes = kScBytes + kMiscFloats * 4 + kFixedBars * 8 + 16 * 4;
   static constexpr int kFit = (kSmemMax - kRingOff - kTailBytes) / (kTileBytes + 16);
@@ -263,6 +267,90 @@ __device__ __forceinline__ uint32_t f16x2_rest(uint32_t a, uint32_t b) {
       : "=r"(d)
       : "r"(a), "r"(b), "r"(0x4c004c00u));
   return d;
+}
+
+// Two fp32 -> e5m2x2 (to nearest even), the low one first; fp16x2 -> two fp32; a - b on fp16 pairs.
+__device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint64_t f16x2_to_f32x2(uint32_t h) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+  return f2pack(lo, hi);
+}
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A pair of codes c, |c| < 2^10, as four e5m2 parts each: c = p0 + (p1 + p2) / 2^8 + p3 / 2^17.
+// e5m2 is fp16's upper byte, so h = fp16(c) is taken apart by integer rounding to that byte (to
+// nearest, halves up) and exact fp16 differences.  In h's units in the last place (2^-24 below its
+// normal numbers) |h| < 2^11: |h - p0| <= 2^7, 2^8 of it is at most 2^14; p1 leaves at most 2^3, three
+// bits, which p2 holds as it is (in units of no less than 2^-16).  p3 is c - h, which fp32 has exactly, to
+// nearest and three bits: off by 2^-15 of c, or by 2^-29 where that is more.  A NaN gets through in
+// p2 and p3.
+// The upper bytes of p0, p1 and p2's halves are their codes; p3 is two codes.
+constexpr float kPartUnit1 = 1.f / (1 << 8), kPartUnit3 = 1.f / (1 << 17);
+__device__ __forceinline__ void decode_parts(uint64_t c, uint32_t (&p)[4]) {
+  float a, b;
+  f2unpack(c, a, b);
+  const uint32_t h = pack_f16(a, b);
+  p[0] = (h + 0x00800080u) & 0xff00ff00u;
+  const uint32_t r = f16x2_mul(f16x2_sub(h, p[0]), 0x5c005c00u);  // 2^8
+  p[1] = (r + 0x00800080u) & 0xff00ff00u;
+  p[2] = f16x2_sub(r, p[1]);
+  f2unpack(ffma2(f16x2_to_f32x2(h), f2pack(-131072.f, -131072.f), mul2(c, f2pack(131072.f, 131072.f))), a, b);
+  p[3] = pack_e5m2(a, b);
+}
+
+// The references of one query head of an e4m3 cache: m, its largest score (log2) so far; e, a power
+// of two that its products of weight (relative to m) and V's factor have not passed; and r = m -
+// delta, the reference of the scores, with a whole delta in [0, kHeadLog2].
+// A code is 2^(score - r) * factor * code, where `code` is one power of two for the 8 heads of a
+// softmax warp: 2^kCodeLog2 / the largest of their e, so that theirs is the largest code.  A head whose
+// products are smaller has its scores' reference lowered by as much (its weights raised), and so its own
+// largest code where the others' is; only below 2^-kHeadLog2 of them does it lose resolution.
+// Weights, codes and sums stay in range: a weight is at most 2^kHeadLog2 on r, and r is rounded up where
+// m is so large that it cannot hold the difference.
+struct DecodeRefs {
+  float m, r, e;
+};
+// Products as powers of two, within [2^-116, 2^126].
+__device__ __forceinline__ uint32_t decode_power(float x) {
+  return max((min(__float_as_uint(x), 0x7e800000u) + 0x7fffffu) & 0x7f800000u, 11u << 23);
+}
+template <class C>
+__device__ __forceinline__ DecodeRefs decode_references(float m, float product, uint32_t &code) {
+  const uint32_t mine = decode_power(product), most = __reduce_max_sync(0xffffffffu, mine);
+  code = ((254u + C::kCodeLog2) << 23) - most;  // 2^kCodeLog2 / most
+  const uint32_t delta = min((most - mine) >> 23, static_cast<uint32_t>(C::kHeadLog2));
+  return {m, __fadd_ru(m, -static_cast<float>(delta)), __uint_as_float(most - (delta << 23))};
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ln(2^m l): l's exponent goes to m first, whose rounding is the result's; with log2(l) alone a large
+// exponent would cost the result's last bits.
+__device__ __forceinline__ float decode_lse(float m, float l) {
+  const uint32_t b = __float_as_uint(l);
+  if (b - 0x00800000u >= 0x7f000000u) return (m + log2f(l)) * 0.69314718055994531f;  // 0, NaN, infinity
+  return ((m + static_cast<float>(static_cast<int>(b >> 23) - 127)) + log2f(__uint_as_float((b & 0x7fffffu) | 0x3f800000u))) *
+         0.69314718055994531f;
 }
 
 // Barrier `id` over `n` threads that also returns whether any of them passed true.
@@ -486,8 +574,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   float *xmax = reinterpret_cast<float *>(smem + C::kMiscOff);    // [2][GB][4]
   float *lpart = xmax + 2 * GB * 4;                               // [2][4][GB]
   float *mstat = lpart + 2 * 4 * GB;                              // [2][GB]
-  float *vmaxw = mstat + 2 * GB;                                  // [kGroups][2][4], read as float4 like xmax
-  float *qscale = vmaxw + 8 * C::kGroups;                         // [2][kGroups]
+  float *vmaxw = mstat + 2 * GB;                                  // e4m3: [2][GB][4], read as float4 like xmax
+  float *refs = vmaxw + 8 * GB;                                   // e4m3: [4][3][GB], a warp's own
+  float *qscale = E4M3 ? refs + 12 * GB : vmaxw;                  // [2][kGroups]
   float *vstat = qscale + 2 * C::kGroups;                         // [2][kGroups]
   static_assert(C::kMiscOff % 16 == 0 && (18 * GB) % 4 == 0, "xmax and vmaxw on 16 bytes");
   uint8_t *ring = smem + C::kRingOff;
@@ -680,8 +769,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     // and a satisfied wait is some 100 cycles of it.  So V and P, usually both there, are
     // looked at by two lanes at once (a wait that may suspend must not be: with lanes on
     // different barriers it sleeps to its limit).
+    constexpr uint32_t kBIsE5m2 = 1u << 10;  // B's format: the weights' parts
     constexpr uint32_t idesc_s = E4M3 ? make_idesc_e4m3(128, C::kQCols, 0, 0) : make_idesc_bf16(128, C::kQCols, 0, 0);
-    constexpr uint32_t idesc_o = E4M3 ? make_idesc_e4m3(128, C::kOCols, 1, 1) : make_idesc_bf16(128, C::kOCols, 1, 1);
+    constexpr uint32_t idesc_o = E4M3 ? make_idesc_e4m3(128, C::kOCols, 1, 1) | kBIsE5m2 : make_idesc_bf16(128, C::kOCols, 1, 1);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t ring0 = smem_u32(ring);
     // K (rows are keys) and Q (rows are heads) are K-major in the same panels.  With 8 bf16
@@ -910,7 +1000,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     constexpr int kH = C::kHeads, kPairs = kH / 2, kSpan = 32 / kH;  // kSpan lanes end up with one head's maximum
     float *xm = xmax + kH * grp * 4;
     uint64_t nm2[kPairs], l2[kPairs];           // minus the reference, and this key's sum of weights
-    float vref = 1.f, vinv = 1.f;     // e4m3: power of two that V's factors are taken relative to; 2^kWeightLog2 / vref
+    float code = 1.f;  // e4m3: of the group's heads (decode_references)
+    float *ref = refs + 3 * w4 * GB + kH * grp + lane / kSpan;  // of head lane / kSpan: m, r and e, GB apart
     bool bad = false, stop = false;
     int n = 0, nred = 0, sv = 1;      // tiles, reductions, ring slot of the tile's V
     uint32_t vph = 0;
@@ -935,6 +1026,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           f = qs * sc[key];
           fv = sc[128 + key];
         }
+        // How far a weight (log2) may go before the references move.  e4m3: the code's limit, or the weight's.
+        const float room = E4M3 ? fminf(C::kCodeLog2 + C::kGrowV - lg2(fabsf(fv * code)), C::kHeadLog2 + C::kGrow) : C::kGrow;
         bad |= !decode_wait(ctx, &bar_s[buf], (n >> 1) & 1, kTagDS);
         __syncwarp();
         tc_fence_after();
@@ -993,62 +1086,84 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           float top = x[0];
 #pragma unroll
           for (int g = 1; g < kH; ++g) top = fmaxf(top, x[g]);
-          grow = top > C::kGrow;
-          if constexpr (E4M3) grow |= fabsf(fv) > vref;
+          grow = top > room;
           grow = bar_any(bar_a, 128, grow || bad);
         }
         if (grow) {
           // The reference moves (or a segment begins) to the maximum over the keys so far.
           float *xr = xm + (nred & 1) * GB * 4;
-          float *vr = vmaxw + grp * 8 + (nred & 1) * 4;
-          ++nred;
           float v[kH];
 #pragma unroll
           for (int g = 0; g < kPairs; ++g) f2unpack(v2[g], v[2 * g], v[2 * g + 1]);
           reduce_columns<kH>(v, [](float a, float b) { return fmaxf(a, b); });
           if (lane % kSpan == 0) xr[lane / kSpan * 4 + w4] = v[0];
-          if constexpr (E4M3) {
-            const uint32_t vm = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
-            if (lane == 0) vr[w4] = __uint_as_float(vm);
-          }
           if (bar_any(bar_b, 128, bad)) {
             stop = true;
             break;
           }
-          float vscale = 1.f;
-          if constexpr (E4M3) {
-            const float4 v4 = *reinterpret_cast<const float4 *>(vr);
-            const uint32_t top = __float_as_uint(fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w)));
-            // The next power of two, within [2^-120, 2^126].
-            const uint32_t up = (min(top, 0x7e800000u) + 0x7fffffu) & 0x7f800000u;
-            uint32_t now = max(up, 7u << 23);
-            if (i > 0) {
-              const uint32_t old = __float_as_uint(vref);
-              now = max(now, old);
-              // old / now, a power of two (or 0 below the normal ones).
-              vscale = __uint_as_float(static_cast<uint32_t>(max(static_cast<int>((127u << 23) + old - now), 0)));
-            }
-            vref = __uint_as_float(now);
-            vinv = __uint_as_float(((254u + C::kWeightLog2) << 23) - now);  // 2^kWeightLog2 / now
-          }
           // Head lane / kSpan's maximum; the lowest number stands in for -inf, so that differences stay defined.
           const float4 m4 = *reinterpret_cast<const float4 *>(xr + lane / kSpan * 4);
           const float mc = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), -3.402823466e38f);
-          float alpha[kH];
+          float alpha[kH];  // what O is multiplied by
+          if constexpr (!E4M3) {
 #pragma unroll
-          for (int g = 0; g < kPairs; ++g) {
-            float a, b;
-            f2unpack(nm2[g], a, b);
-            float m0 = __shfl_sync(0xffffffffu, mc, 2 * g * kSpan), m1 = __shfl_sync(0xffffffffu, mc, (2 * g + 1) * kSpan);
-            if (i > 0) {
-              m0 = fmaxf(m0, -a);
-              m1 = fmaxf(m1, -b);
+            for (int g = 0; g < kPairs; ++g) {
+              float a, b;
+              f2unpack(nm2[g], a, b);
+              float m0 = __shfl_sync(0xffffffffu, mc, 2 * g * kSpan), m1 = __shfl_sync(0xffffffffu, mc, (2 * g + 1) * kSpan);
+              if (i > 0) {
+                m0 = fmaxf(m0, -a);
+                m1 = fmaxf(m1, -b);
+              }
+              alpha[2 * g] = ex2(-a - m0);
+              alpha[2 * g + 1] = ex2(-b - m1);
+              nm2[g] = f2pack(-m0, -m1);
+              if (i > 0) l2[g] = mul2(l2[g], f2pack(alpha[2 * g], alpha[2 * g + 1]));
             }
-            alpha[2 * g] = ex2(-a - m0);
-            alpha[2 * g + 1] = ex2(-b - m1);
-            nm2[g] = f2pack(-m0, -m1);
-            if (i > 0) l2[g] = mul2(l2[g], f2pack(alpha[2 * g], alpha[2 * g + 1]));
+          } else {
+            // The tile's largest products relative to the new maxima: a value row counts with the weight
+            // it has, and one much larger than the others that is hardly seen leaves their resolution alone.
+            DecodeRefs old = {mc, 0.f, 0.f};
+            if (i > 0) old = {ref[0], ref[GB], ref[2 * GB]};
+            const float mx = fmaxf(mc, old.m);
+            float t[kH];
+#pragma unroll
+            for (int g = 0; g < kPairs; ++g) {
+              float a, b;
+              f2unpack(v2[g], a, b);
+              t[2 * g] = ex2(a - __shfl_sync(0xffffffffu, mx, 2 * g * kSpan)) * fabsf(fv);
+              t[2 * g + 1] = ex2(b - __shfl_sync(0xffffffffu, mx, (2 * g + 1) * kSpan)) * fabsf(fv);
+            }
+            reduce_columns<kH>(t, [](float a, float b) { return fmaxf(a, b); });
+            float *vr = vmaxw + (kH * grp + (nred & 1) * GB) * 4;
+            if (lane % kSpan == 0) vr[lane / kSpan * 4 + w4] = t[0];
+            bar_any(bar_b, 128, false);
+            const float4 t4 = *reinterpret_cast<const float4 *>(vr + lane / kSpan * 4);
+            uint32_t next;
+            const DecodeRefs now = decode_references<C>(
+                mx, fmaxf(fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)), old.e * ex2(old.m - mx)), next);
+            // O goes by the codes, l by the weights.
+            const float up = static_cast<float>(static_cast<int>(next >> 23) - static_cast<int>(__float_as_uint(code) >> 23));
+            const float of_l = ex2(old.r - now.r), of_o = ex2((old.r - now.r) + up);
+            code = __uint_as_float(next);
+            __syncwarp();
+            if (lane % kSpan == 0) {
+              ref[0] = now.m;
+              ref[GB] = now.r;
+              ref[2 * GB] = now.e;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < kPairs; ++g) {
+              nm2[g] = f2pack(-__shfl_sync(0xffffffffu, now.r, 2 * g * kSpan), -__shfl_sync(0xffffffffu, now.r, (2 * g + 1) * kSpan));
+              if (i > 0) {
+                alpha[2 * g] = __shfl_sync(0xffffffffu, of_o, 2 * g * kSpan);
+                alpha[2 * g + 1] = __shfl_sync(0xffffffffu, of_o, (2 * g + 1) * kSpan);
+                l2[g] = mul2(l2[g], f2pack(__shfl_sync(0xffffffffu, of_l, 2 * g * kSpan), __shfl_sync(0xffffffffu, of_l, (2 * g + 1) * kSpan)));
+              }
+            }
           }
+          ++nred;
           if (i > 0) {
             // O holds tiles of this segment on the old reference: bring it to the new one.
             if constexpr (C::kPvBar) {
@@ -1066,7 +1181,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
               tmem_ld_n<kH>(to + part * GB, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < kH; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (alpha[e] * vscale));
+              for (int e = 0; e < kH; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[e]);
               tmem_st_n<kH>(to + part * GB, o);
             }
             tmem_wait_st();
@@ -1086,23 +1201,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             part[0][g] = pack_bf16(a, b);
             part[1][g] = pack_bf16(a - bf16_lo(part[0][g]), b - bf16_hi(part[0][g]));
           } else {
-            const float fw = fv * vinv;
-            float wa, wb;
-            f2unpack(mul2(f2pack(a, b), f2pack(fw, fw)), wa, wb);
-            uint32_t r = pack_f16(wa, wb);
+            const float fc = fv * code;
+            uint32_t four[4];
+            decode_parts(mul2(f2pack(a, b), f2pack(fc, fc)), four);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-              const uint16_t c = f16x2_to_e4m3x2(r);
-              part[k][g] = c;
-              if (k < 2) r = f16x2_rest(r, e4m3x2_to_f16x2(c));
-            }
+            for (int k = 0; k < 4; ++k) part[k][g] = four[k];
           }
         }
-        if constexpr (E4M3) {  // two codes a word so far: four
+        if constexpr (E4M3 && kPairs > 1) {  // the codes of two pairs a word
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int g = 0; g < kPairs / 2; ++g) part[k][g] = part[k][2 * g] | (part[k][2 * g + 1] << 16);
+            for (int g = 0; g < kPairs / 2; ++g)
+              part[k][g] = __byte_perm(part[k][2 * g], part[k][2 * g + 1], k < 3 ? 0x7531 : 0x5410);
         }
         constexpr int kPartBytes = kH * C::kElem;  // of this thread, per part
         if constexpr (kPartBytes == 16) {
@@ -1112,7 +1223,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
                          part[k][3]);
         } else if constexpr (kPartBytes == 8 && E4M3) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
+          for (int k = 0; k < 4; ++k) {
             const int byte = k * GB + kH * grp;
             st_shared_v2(pb + swizzled<C::kPRow>(key, byte & ~15) + (byte & 8), part[k][0], part[k][1]);
           }
@@ -1125,9 +1236,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         } else {
           const uint32_t at = pb + swizzled<C::kPRow>(key, 0);
           if constexpr (kH == 4)
-            st_shared_v4(at, part[0][0], part[1][0], part[2][0], 0u);
-          else
-            st_shared_v2(at, part[0][0] | (part[1][0] << 16), part[2][0]);
+            st_shared_v4(at, part[0][0], part[1][0], part[2][0], part[3][0]);
+          else  // two heads: two codes of each part
+            st_shared_v2(at, __byte_perm(part[0][0], part[1][0], 0x7531), __byte_perm(part[2][0], part[3][0], 0x5431));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1153,7 +1264,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
       if (w4 == 0 && lane == 0) {
 #pragma unroll
         for (int g = 0; g < kH; ++g) mstat[ob * GB + kH * grp + g] = -m[g];
-        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = vref * (1.f / (1 << C::kWeightLog2));
+        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = __uint_as_float((254u << 23) - __float_as_uint(code));  // 1 / code
       }
       __syncwarp();
       if (lane == 0) {
@@ -1212,13 +1323,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         const float *lp = lpart + ob * 4 * GB + gc + (lane & (kH - 1));
         const float lt = (lp[0] + lp[GB]) + (lp[2 * GB] + lp[3 * GB]);
         const float mh = mstat[ob * GB + gc + (lane & (kH - 1))];
-        float mul = E4M3 ? vstat[ob * C::kGroups + gc / kH] : 1.f;
-        if (whole) mul = __fdividef(mul, lt);
+        const float mul = whole ? __fdividef(1.f, lt) : 1.f;
+        const float unit = E4M3 ? vstat[ob * C::kGroups + gc / kH] : 1.f;  // of a code
         if ((warp & 3) == 0 && lane < kH && gc + lane < ng) {
           if (!whole)
             p.part_ml[slot * GB + gc + lane] = make_float2(mh, lt);
           else if (p.lse)
-            p.lse[row0 + gc + lane] = (mh + log2f(lt)) * 0.69314718055994531f;
+            p.lse[row0 + gc + lane] = decode_lse(mh, lt);
         }
         tmem_wait_ld();
         uint16_t *po = p.o + (row0 + gc) * D + f;
@@ -1227,10 +1338,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         for (int e = 0; e < kH; ++e) {
           float v = __uint_as_float(o[0][e]);
           if constexpr (E4M3)
-            v += (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e]) * 0.0625f) * 0.0625f;
+            v += (__uint_as_float(o[1][e]) + __uint_as_float(o[2][e])) * kPartUnit1 + __uint_as_float(o[3][e]) * kPartUnit3;
           else if (fabsf(v) != INFINITY)  // an infinite value: the low part's product with it may be NaN
             v += __uint_as_float(o[1][e]);
           v *= __shfl_sync(0xffffffffu, mul, e);
+          if constexpr (E4M3) v *= unit;  // apart: their product may lie below fp32's range
           if (gc + e < ng) {
             if (whole)
               po[e * D] = static_cast<uint16_t>(pack_bf16(v, 0.f));
@@ -1335,7 +1447,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __gr
   const float inv = __fdividef(1.f, L);
   *reinterpret_cast<uint2 *>(p.o + out * D + 4 * col) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (col == 0 && p.lse) p.lse[out] = (M + log2f(L)) * 0.69314718055994531f;
+  if (col == 0 && p.lse) p.lse[out] = decode_lse(M, L);
 }
 
 }  // namespace fa

@@ -1,0 +1,119 @@
+"""fa_decode over e4m3 caches whose weights, values and queries span a wide range."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from cache_bounds import aimed, check_tight, copies, decode_tight, run
+from cache_helpers import DEV, Cache
+from io_aware_exact_23_b200 import binding as fa
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(n, H, d, seed, mean=0.0, mult=1.0):
+    g = torch.Generator(device="cpu").manual_seed(seed)
+    return (mean + mult * torch.randn(n, H, d, generator=g)).to(DEV)
+
+
+# --------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("nats", [9, 12, 15, 18])
+@pytest.mark.parametrize("B", [1, 400])
+def test_many_keys_below_one(B, nats, e4m3):
+    """One key far above 100000 others whose weights count together: values with a common mean, the
+    first one's own value zero.  In one CTA each (B = 400) and split over many."""
+    n, d = 100000, 64
+    c = Cache([n], 1, d, 64, e4m3, seed=1, fill=False)
+    s = rows(n, 1, 1, 2, mult=0.2).flatten()
+    s[0] = nats
+    q = aimed(c, s, 8)
+    v = rows(n, 1, d, 3, mean=1.0, mult=0.25)
+    v[0] = 0
+    c.put(c.v, c.vs, 0, torch.arange(n, device=DEV), v.to(torch.bfloat16))
+    ref = decode_tight(c, q, 1.0)
+    copies(c, B)
+    o, L = run(fa, c, q[None].repeat(B, 1, 1))
+    for b in {0, B // 2, B - 1}:
+        check_tight(o[b], L[b], ref, f"{nats} nats, row {b}")
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 8, 16, 32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("times", [2.0**8, 1e4, 1e6, 1e20])
+def test_one_large_value_row(times, d, G):
+    """A value row `times` the others whose own weight is next to nothing."""
+    n = 4096
+    c = Cache([n], 2, d, 16, True, seed=4, fill=False)
+    s = rows(n, 1, 1, 5).flatten()
+    s[777] = -60.0
+    q = aimed(c, s, G)
+    v = rows(n, 2, d, 6, mean=0.5)
+    v[777] *= times
+    c.put(c.v, c.vs, 0, torch.arange(n, device=DEV), v.to(torch.bfloat16))
+    ref = decode_tight(c, q, 1.0)
+    o, L = run(fa, c, q[None])
+    check_tight(o[0], L[0], ref, f"times {times}")
+
+
+@pytest.mark.parametrize("G", [1, 4, 5, 12, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_factors_of_every_size(d, G):
+    """Value rows between 2^-20 and 2^20 of each other, some of them zero, some factors negative,
+    weights between 1 and e^-30."""
+    for lens in ([1500], [100], [1]):
+        n = lens[0]
+        c = Cache(lens, 2, d, 32, True, seed=7, fill=False)
+        g = torch.Generator(device="cpu").manual_seed(8)
+        s = torch.randint(-30, 1, (n,), generator=g).float().to(DEV)
+        q = aimed(c, s, G)
+        v = rows(n, 2, d, 9) * torch.exp2(torch.randint(-20, 21, (n, 2, 1), generator=g).float()).to(DEV)
+        v[5::9] = 0
+        c.put(c.v, c.vs, 0, torch.arange(n, device=DEV), v.to(torch.bfloat16))
+        c.vs[::2] = -c.vs[::2]
+        ref = decode_tight(c, q, 1.0)
+        o, L = run(fa, c, q[None])
+        check_tight(o[0], L[0], ref, f"{n} keys")
+
+
+@pytest.mark.parametrize("mult", [1e-33, 1e-20, 1e20, 1e33])
+def test_values_near_the_ends_of_the_type(mult):
+    n, d = 600, 64
+    for e4m3 in (False, True):
+        c = Cache([n], 1, d, 16, e4m3, seed=10, fill=False)
+        q = aimed(c, rows(n, 1, 1, 11).flatten(), 4)
+        v = (rows(n, 1, d, 12) * mult).to(torch.bfloat16)
+        c.put(c.v, c.vs, 0, torch.arange(n, device=DEV), v)
+        ref = decode_tight(c, q, 1.0)
+        o, L = run(fa, c, q[None])
+        check_tight(o[0], L[0], ref, f"{mult}")
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_climb_while_values_shrink(d, sign):
+    """The largest weight and the largest product of weight and factor are different keys, and both keep moving."""
+    n = 1300
+    c = Cache([n], 1, d, 16, True, seed=13, fill=False)
+    at = torch.arange(n, device=DEV)
+    q = aimed(c, torch.floor(sign * at.float() / 8), 8)
+    v = rows(n, 1, d, 14, mean=1.0) * torch.exp2(-sign * (at // 11).float())[:, None, None] * 2.0**(60 * sign)
+    c.put(c.v, c.vs, 0, at, v.to(torch.bfloat16))
+    ref = decode_tight(c, q, 1.0)
+    o, L = run(fa, c, q[None])
+    check_tight(o[0], L[0], ref)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G", [1, 2, 4, 8, 16, 32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_ordinary_rows(d, G, e4m3):
+    """Every instance on random rows, to the bound that bf16 outputs allow."""
+    lens = [1, 130, 2000, 0, 515]
+    c = Cache(lens, 2, d, 64, e4m3, seed=15 + G)
+    g = torch.Generator(device="cpu").manual_seed(G)
+    q = torch.randn(5, 2 * G, d, generator=g).to(torch.bfloat16).to(DEV)
+    o, L = run(fa, c, q, scale=0.3)
+    for b, n in enumerate(lens):
+        if n:
+            check_tight(o[b], L[b], decode_tight(c, q[b], 0.3, b=b), f"sequence {b}")
