@@ -86,8 +86,8 @@ typedef struct {
  * FA_CACHE_BF16 copies.  FA_CACHE_E4M3 quantises each (token, head) row x:
  *   factor = max(max|x|, 1e-30) / 448,  code = e4m3(x / factor),
  * in fp32 with IEEE division, rounded to nearest even, so that the row's largest
- * element becomes 448, the largest e4m3 value; a row that holds an infinity or
- * NaN comes back as NaN there.
+ * element becomes 448, the largest e4m3 value.  The factor of a row that holds an
+ * infinity or NaN is one too, and the row is NaN throughout: its codes are 0 or NaN.
  * The pages written by one call must not be shared: two sequences that own the
  * same row leave either's values, or a mix, in it.
  */
@@ -99,7 +99,7 @@ int fa_cache_append(const fa_paged_cache *cache, const void *k_new, const void *
  * Read sequences back as the contiguous bf16 [B, H * rep, N, d] tensors that fa_fwd
  * takes: head h of the cache becomes heads h * rep .. h * rep + rep - 1 (rep query
  * heads that share it).  Row n >= seq_lens[b] is zero; positions from N on are left
- * out.  e4m3 rows are code * factor, rounded once to bf16.  k_out or v_out NULL
+ * out.  e4m3 rows are code * factor in fp32, rounded to bf16 (0 * infinity is NaN).  k_out or v_out NULL
  * leaves that one out.  B * H * rep * N * d < 2^31, as for fa_fwd.
  */
 int fa_cache_gather(const fa_paged_cache *cache, void *k_out, void *v_out, int rep, int N,
@@ -121,7 +121,8 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int H, int d);
  * log) or NULL.  Hq is a multiple of H.  o may be q itself (a row of q is last read
  * before its row of o is written), and overlaps nothing else.  A sequence of length 0
  * gets o = 0 and lse = -inf.  Scores, statistics and sums are fp32; o is rounded once, to bf16.
- * Before that, weights enter the product with V with 16 bits (bf16), or, times V's factor, to within
+ * A visible row of FA_CACHE_E4M3 whose factor is not finite makes its heads' o NaN.
+ * Before that rounding, weights enter the product with V with 16 bits (bf16), or, times V's factor, to within
  * 2^-15 of themselves or 2^-32 of the largest such product of their head (FA_CACHE_E4M3); its sums are
  * the tensor core's, which drop what lies below fp32's last place: a part of 2^-23 at most for every 16
  * (bf16) or 32 (e4m3) positions that one block takes of a sequence.

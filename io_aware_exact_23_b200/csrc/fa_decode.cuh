@@ -1023,8 +1023,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           const int st = n % C::kScStages;
           bad |= !decode_wait(ctx, &bar_sc[st], (n / C::kScStages) & 1, kTagDSc);
           const float *sc = reinterpret_cast<const float *>(smem + C::kScOff + st * 1024);
-          f = qs * sc[key];
-          fv = sc[128 + key];
+          // x + 0 x: an infinite factor counts as NaN.  Of an appended row its codes are 0 and NaN, and
+          // elsewhere it would give a score or a weight of one sign only where its codes have both.
+          f = qs * __fmaf_rn(sc[key], 0.f, sc[key]);
+          fv = __fmaf_rn(sc[128 + key], 0.f, sc[128 + key]);
         }
         // How far a weight (log2) may go before the references move.  e4m3: the code's limit, or the weight's.
         const float room = E4M3 ? fminf(C::kCodeLog2 + C::kGrowV - lg2(fabsf(fv * code)), C::kHeadLog2 + C::kGrow) : C::kGrow;

@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from cache_bounds import run
+from cache_bounds import check_tight, decode_tight, run
 from cache_helpers import DEV, Cache
 from io_aware_exact_23_b200 import binding as fa
 
@@ -49,6 +49,49 @@ def test_gather_multiplies_every_code():
     assert fa.fa_device_status() == 0
     assert torch.isnan(out[0, 0, :2]).all() and (out[0, 0, 2:] == 0).all()
     assert torch.signbit(out[0, 0, 3]).all() and not torch.signbit(out[0, 0, 2]).any()
+
+
+# ---------------------------------------------------- rows of the cache, in decode
+@pytest.mark.parametrize("G", [1, 4, 8, 20])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_decode_of_a_quantised_row_that_was_not_finite(value, which, d, G):
+    """Appended to cache head 1 of sequence 1: its query heads are NaN, all others hold."""
+    lens = [300, 300, 77]
+    c = Cache(lens, 2, d, 16, True, seed=3)
+    q = queries(3, 2 * G, d)
+    new = [torch.randn(3, 2, d, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    new["kv".index(which)][1, 1, 17] = value
+    for n in (150, 300):  # the row in the middle of its sequence, and one at its end
+        c.lens[1] = n
+        fa.fa_cache_append(new[0], new[1], c.k, c.v, **c.args)
+        c.lens[1] = 300
+        o, L = run(fa, c, q, scale=0.2)
+        assert torch.isnan(o[1, G:]).all()
+        assert torch.isnan(L[1, G:]).all() if which == "k" else torch.isfinite(L[1, G:]).all()
+        for b in range(3):
+            ref = decode_tight(c, q[b], 0.2, b=b)
+            keep = slice(0, G) if b == 1 else slice(None)
+            check_tight(o[b, keep], L[b, keep], tuple(x[keep] for x in ref), f"sequence {b}")
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("at", [0, 100, 700, 1499])
+def test_decode_of_a_factor_that_is_not_finite(at, value):
+    """A visible row under such a factor, whatever its codes: NaN in every feature of its heads."""
+    for where in ("ks", "vs"):
+        c = Cache([1500, 300], 2, 64, 64, True, seed=4)
+        page, off = c.where(0, torch.tensor([at], device=DEV))
+        getattr(c, where)[page[0], 1, off[0]] = value
+        c.v[page[0], 1, off[0], ::2] = 0
+        q = queries(2, 8, 64)
+        o, _ = run(fa, c, q, scale=0.2)
+        assert torch.isnan(o[0, 4:]).all()
+        assert torch.isfinite(o[0, :4]).all() and torch.isfinite(o[1]).all()
+        c.lens[0] = at  # the row is no longer visible
+        o, _ = run(fa, c, q, scale=0.2)
+        assert torch.isfinite(o).all()
 
 
 # ------------------------------------------------------------ parts of a sequence
