@@ -121,7 +121,8 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int H, int d);
  * log) or NULL.  Hq is a multiple of H.  o may be q itself (a row of q is last read
  * before its row of o is written), and overlaps nothing else.  A sequence of length 0
  * gets o = 0 and lse = -inf.  Scores, statistics and sums are fp32; o is rounded once, to bf16.
- * A visible row of FA_CACHE_E4M3 whose factor is not finite makes its heads' o NaN.
+ * FA_CACHE_E4M3: an element of q counts to within 2^-22 of the largest of its row; a visible cache row
+ * whose factor is not finite makes its heads' o NaN.
  * Before that rounding, weights enter the product with V with 16 bits (bf16), or, times V's factor, to within
  * 2^-15 of themselves or 2^-32 of the largest such product of their head (FA_CACHE_E4M3); its sums are
  * the tensor core's, which drop what lies below fp32's last place: a part of 2^-23 at most for every 16

@@ -28,8 +28,8 @@
 // idle; the idle columns carry the low part of the operand that has to be rounded:
 // * bf16: P = hi + lo, both bf16 (16 significant bits), as 2 GB columns of O^T;
 // * e4m3: codes are multiplied as they are (kind::f8f6f4), the factor of K goes into the
-//   score, that of V into the weight.  q (8 bits, scaled by one power of two per 8 heads) is
-//   hi + lo / 16 in e4m3, exact to 2^-20 of its largest element.  A weight times V's factor is
+//   score, that of V into the weight.  q (8 bits, a power of two taken out of each head) is
+//   hi + lo / 32 in e4m3, exact to 2^-22 of the head's largest element.  A weight times V's factor is
 //   four e5m2 parts (decode_parts): off by 2^-15 of itself at most, or by 2^-32 of the head's
 //   largest such product, so that many keys far below one still count (three e4m3 parts of
 //   fp16's 11 bits stopped at 2^-20 of it).
@@ -116,9 +116,9 @@ struct DecodeCfg {
   static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kRingOff = (kQOff + 2 * kQBytes + 1023) / 1024 * 1024;
   // Behind the ring: factors, then floats xmax[2][GB][4], lpart[2][4][GB], mstat[2][GB], of e4m3
-  // vmax[2][GB][4] and refs[4][3][GB], and qscale[2][kGroups], vstat[2][kGroups], then barriers and words.
+  // vmax[2][GB][4] and refs[4][3][GB], and qscale[2][GB], vstat[2][kGroups], then barriers and words.
   static constexpr int kScBytes = E4M3 ? kScStages * 1024 : 0;
-  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + (E4M3 ? 20 * GB : 0) + 4 * kGroups;
+  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + (E4M3 ? 22 * GB : 0) + 4 * kGroups;
   static constexpr int kFixedBars = 20 + 2 * kScStages;
   static constexpr int kTailBytes = kScBytes + kMiscFloats * 4 + kFixedBars * 8 + 16 * 4;
   static constexpr int kFit = (kSmemMax - kRingOff - kTailBytes) / (kTileBytes + 16);
@@ -260,15 +260,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
-// 16 (a - b) on fp16 pairs.
-__device__ __forceinline__ uint32_t f16x2_rest(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
-      : "=r"(d)
-      : "r"(a), "r"(b), "r"(0x4c004c00u));
-  return d;
-}
-
 // Two fp32 -> e5m2x2 (to nearest even), the low one first; fp16x2 -> two fp32; a - b on fp16 pairs.
 __device__ __forceinline__ uint32_t pack_e5m2(float lo, float hi) {
   uint16_t r;
@@ -576,8 +567,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   float *mstat = lpart + 2 * 4 * GB;                              // [2][GB]
   float *vmaxw = mstat + 2 * GB;                                  // e4m3: [2][GB][4], read as float4 like xmax
   float *refs = vmaxw + 8 * GB;                                   // e4m3: [4][3][GB], a warp's own
-  float *qscale = E4M3 ? refs + 12 * GB : vmaxw;                  // [2][kGroups]
-  float *vstat = qscale + 2 * C::kGroups;                         // [2][kGroups]
+  float *qscale = E4M3 ? refs + 12 * GB : vmaxw;                  // e4m3: [2][GB]
+  float *vstat = E4M3 ? qscale + 2 * GB : vmaxw;                  // e4m3: [2][kGroups]
   static_assert(C::kMiscOff % 16 == 0 && (18 * GB) % 4 == 0, "xmax and vmaxw on 16 bytes");
   uint8_t *ring = smem + C::kRingOff;
 
@@ -867,18 +858,24 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   } else if (warp == C::kQWarp) {
     // ---------------------------------------------------------------- Q rows
     // Rows of the segment's query heads into swizzled shared memory, kHeads at a time; the next
-    // ones (of this segment or the next) are read meanwhile.  Lane's piece i is 16 bytes, the
+    // ones (of this segment or the next) are read meanwhile.  A lane's piece i is 16 bytes, of bf16 the
     // (32 i + lane)th of the rows.  Rows past the last head are 0.
     constexpr int kPerRow = D / 8, kAll = C::kHeads * kPerRow, kPieces = (kAll + 31) / 32;
+    // (e4m3: of kLanes lanes to a row, so that its maximum takes few shuffles: 64 ragged sequences up to
+    // 4096 with 32 heads 26.5 us, 28.3 with the pieces in order.)
+    constexpr int kLanes = 32 / C::kHeads;
+    auto row_of = [&](int i) { return E4M3 ? lane / kLanes : (32 * i + lane) / kPerRow; };
+    auto piece_of = [&](int i) { return E4M3 ? i * kLanes + lane % kLanes : (32 * i + lane) % kPerRow; };
+    auto there = [&](int i) { return E4M3 ? piece_of(i) < kPerRow : 32 * i + lane < kAll; };
     uint4 w[kPieces];
     auto load = [&](int c) {
       const int g0 = wk.blk * GB + C::kHeads * c;
       const uint16_t *src = p.q + (static_cast<long long>(wk.b) * p.Hq + wk.h * p.G + g0) * D;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int at = 32 * i + lane;
         w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (wk.rem > 0 && at < kAll && g0 + at / kPerRow < p.G) w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + at);
+        if (wk.rem > 0 && there(i) && g0 + row_of(i) < p.G)
+          w[i] = __ldg(reinterpret_cast<const uint4 *>(src) + row_of(i) * kPerRow + piece_of(i));
       }
     };
     bool ok = true;
@@ -898,16 +895,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         if constexpr (!E4M3) {
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
-            const int row = C::kHeads * c + (32 * i + lane) / kPerRow, in = (32 * i + lane) % kPerRow;
-            if (kAll % 32 != 0 && 32 * i + lane >= kAll) break;
+            const int row = C::kHeads * c + row_of(i), in = piece_of(i);
+            if (!there(i)) break;
             st_shared_v4(dst + (in >> 3) * (C::kQRows * 128) + swizzled<128>(row, (in & 7) * 16), v[i].x, v[i].y, v[i].z,
                          v[i].w);
           }
         } else {
-          // Scale the rows by the power of two that brings their largest element into
-          // [128, 256), then split: hi = e4m3(x), lo = e4m3(16 (x - hi)) (bf16 values are
-          // fp16 values in that range).  A row's scores are off by at most 2^-20 of the
-          // group's largest.
+          // Scale each row by the power of two that brings its largest element into
+          // [128, 256), then split: hi = e4m3(x), lo = e4m3(32 (x - hi)) (bf16 values are
+          // fp16 values in that range, |x - hi| is at most 8).  An element is off by at most 2^-22 of its
+          // row's largest.  (One scale for 8 rows would make a head's error another's affair, a NaN included.)
           uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
@@ -915,13 +912,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             const uint32_t b = __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu);
             top = __vmaxu2(top, __vmaxu2(a, b));
           }
-          top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-          // The largest element is in [2^(e-127), 2^(e-126)); x * 2^(134 - e).  An infinity or
-          // NaN (e = 255) makes every score of the group NaN.
-          const int e0 = static_cast<int>(top >> 7), e = min(max(e0, 16), 250);
+          top = max(top >> 16, top & 0xffffu);
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // The row's largest element is in [2^(e-127), 2^(e-126)); x * 2^(134 - e).  An infinity or
+          // NaN (e = 255) makes every score of the head NaN.
+          const int e0 = static_cast<int>(top >> 7), e = min(max(e0, 16), 250), row = C::kHeads * c + row_of(0);
           const float up = __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
-          if (lane == 0)
-            qscale[qb * C::kGroups + c] =
+          if (lane % kLanes == 0)
+            qscale[qb * GB + row] =
                 __uint_as_float(e0 == 255 ? 0x7fc00000u : static_cast<uint32_t>(e - 7) << 23) * p.scale_log2;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
@@ -931,12 +930,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
             for (int k = 0; k < 4; ++k) {
               const uint32_t r = pack_f16(bf16_lo(words[k]) * up, bf16_hi(words[k]) * up);
               const uint16_t hi = f16x2_to_e4m3x2(r);
-              const uint16_t lo = f16x2_to_e4m3x2(f16x2_rest(r, e4m3x2_to_f16x2(hi)));
+              const uint16_t lo = f16x2_to_e4m3x2(f16x2_mul(f16x2_sub(r, e4m3x2_to_f16x2(hi)), 0x50005000u));  // 32
               part[0][k >> 1] |= static_cast<uint32_t>(hi) << (16 * (k & 1));
               part[1][k >> 1] |= static_cast<uint32_t>(lo) << (16 * (k & 1));
             }
-            const int row = C::kHeads * c + (32 * i + lane) / kPerRow, byte = (32 * i + lane) % kPerRow * 8;
-            if (kAll % 32 != 0 && 32 * i + lane >= kAll) break;
+            const int byte = piece_of(i) * 8;
+            if (!there(i)) break;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               st_shared_v2(dst + swizzled<C::kPanelRow>(k * GB + row, byte & ~15) + (byte & 8), part[k][0], part[k][1]);
@@ -1007,25 +1006,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     uint32_t vph = 0;
     for (int seg = 0; wk.rem > 0 && !stop; ++seg) {
       const int run = wk.run(), qb = seg & 1;
-      float qs = p.scale_log2;
-      if constexpr (E4M3) {
-        bad |= !decode_wait(ctx, &bar_q[qb], (seg >> 1) & 1, kTagDQ);
-        qs = qscale[qb * C::kGroups + grp];
-      }
+      const float *qs = qscale + qb * GB + kH * grp;  // e4m3: scale and what was taken out of q, per head
+      if constexpr (E4M3) bad |= !decode_wait(ctx, &bar_q[qb], (seg >> 1) & 1, kTagDQ);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) nm2[i] = l2[i] = 0ull;
 #pragma unroll 1
       for (int i = 0; i < run; ++i, ++n) {
         const int buf = n & 1;
         const int pos0 = (wk.tile0 + wk.off + i) * 128;
-        float f = qs, fv = 1.f;
+        float fk = 1.f, fv = 1.f;
         if constexpr (E4M3) {  // the factors are there first, as a rule
           const int st = n % C::kScStages;
           bad |= !decode_wait(ctx, &bar_sc[st], (n / C::kScStages) & 1, kTagDSc);
           const float *sc = reinterpret_cast<const float *>(smem + C::kScOff + st * 1024);
           // x + 0 x: an infinite factor counts as NaN.  Of an appended row its codes are 0 and NaN, and
           // elsewhere it would give a score or a weight of one sign only where its codes have both.
-          f = qs * __fmaf_rn(sc[key], 0.f, sc[key]);
+          fk = __fmaf_rn(sc[key], 0.f, sc[key]);
           fv = __fmaf_rn(sc[128 + key], 0.f, sc[128 + key]);
         }
         // How far a weight (log2) may go before the references move.  e4m3: the code's limit, or the weight's.
@@ -1047,15 +1043,22 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           for (int g = 0; g < kPairs; ++g) {
             v2[g] = f2pack(__uint_as_float(hi[2 * g]), __uint_as_float(hi[2 * g + 1]));
             if constexpr (E4M3)
-              v2[g] = ffma2(f2pack(__uint_as_float(lo[2 * g]), __uint_as_float(lo[2 * g + 1])), f2pack(0.0625f, 0.0625f),
+              v2[g] = ffma2(f2pack(__uint_as_float(lo[2 * g]), __uint_as_float(lo[2 * g + 1])), f2pack(0.03125f, 0.03125f),
                             v2[g]);
           }
+        }
+        // Scores in the log2 domain, rounded here: a fused multiply-subtract below would be
+        // off from the maximum by the rounding of a product, however large that is.
+#pragma unroll
+        for (int g = 0; g < kPairs; ++g) {
+          uint64_t f = f2pack(p.scale_log2, p.scale_log2);
+          if constexpr (E4M3) f = mul2(f2pack(fk, fk), reinterpret_cast<const uint64_t *>(qs)[g]);
+          v2[g] = mul2(v2[g], f);
         }
         if (pos0 < wk.first || pos0 + 128 > wk.len) {
           const int pos = pos0 + key;
           const bool valid = pos >= wk.first && pos < wk.len;
           if (!valid) {
-            f = 1.f;
             fv = 0.f;
 #pragma unroll
             for (int g = 0; g < kPairs; ++g) v2[g] = f2pack(-INFINITY, -INFINITY);
@@ -1076,10 +1079,6 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           }
           __syncwarp();
         }
-        // Scores in the log2 domain, rounded once here: a fused multiply-subtract below would be
-        // off from the maximum by the rounding of a product, however large that is.
-#pragma unroll
-        for (int g = 0; g < kPairs; ++g) v2[g] = mul2(v2[g], f2pack(f, f));
         float x[kH];  // log2 of the weights
         bool grow = true;
         if (i > 0) {

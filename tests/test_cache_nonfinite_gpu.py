@@ -94,6 +94,25 @@ def test_decode_of_a_factor_that_is_not_finite(at, value):
         assert torch.isfinite(o).all()
 
 
+# ----------------------------------------------------------------- queries
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G", [2, 4, 8, 24])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_a_query_head_that_is_not_finite_is_alone(value, G, e4m3):
+    for d in (64, 128):
+        c = Cache([300, 40], 2, d, 16, e4m3, seed=5)
+        q = queries(2, 2 * G, d)
+        refs = [decode_tight(c, q[b], 0.2, b=b) for b in range(2)]
+        bad = (0, G - 1), (1, G)
+        for b, h in bad:
+            q[b, h, 3] = value
+        o, L = run(fa, c, q, scale=0.2)
+        for b, h in bad:
+            assert torch.isnan(o[b, h]).all() and torch.isnan(L[b, h])
+            keep = [i for i in range(2 * G) if i != h]
+            check_tight(o[b, keep], L[b, keep], tuple(x[keep] for x in refs[b]), f"sequence {b}")
+
+
 # ------------------------------------------------------------ parts of a sequence
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("B", [1, 400])

@@ -117,3 +117,23 @@ def test_ordinary_rows(d, G, e4m3):
     for b, n in enumerate(lens):
         if n:
             check_tight(o[b], L[b], decode_tight(c, q[b], 0.3, b=b), f"sequence {b}")
+
+
+# ----------------------------------------------------------------- queries
+@pytest.mark.parametrize("G", [2, 4, 8, 24])
+@pytest.mark.parametrize("d", [64, 128])
+def test_heads_of_every_size(d, G):
+    """Query heads between 2^-14 and 2^6 of each other: each is as exact as if it were alone."""
+    n = 700
+    c = Cache([n], 2, d, 16, True, seed=20)
+    g = torch.Generator(device="cpu").manual_seed(21)
+    size = torch.exp2(torch.randint(-14, 7, (2 * G, 1), generator=g).float())
+    q = (torch.randn(2 * G, d, generator=g) * size).to(torch.bfloat16).to(DEV)
+    ref = decode_tight(c, q, 1.0)
+    o, L = run(fa, c, q[None])
+    check_tight(o[0], L[0], ref)
+    for h in (0, G):  # the first head of either cache head, next to ones 2^20 times it
+        q2 = q.clone()
+        q2[h + 1] = (torch.randn(d, generator=g) * 2.0**20 * float(size[h])).to(torch.bfloat16)
+        o2, L2 = run(fa, c, q2[None])
+        check_tight(o2[0, h:h + 1], L2[0, h:h + 1], tuple(x[h:h + 1] for x in ref), f"head {h}")
