@@ -8,6 +8,7 @@ raises at import: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -523,6 +524,9 @@ def fa_decode(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, 
              workspace.data_ptr(), workspace.numel())
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
 class KVCache:
     """Allocating convenience wrapper of a paged cache: its tensors and the calls on them.
 
@@ -541,19 +545,21 @@ class KVCache:
     def append(self, k_new, v_new, block_table, seq_lens, cu_new=None, stream=None) -> None:
         fa_cache_append(k_new, v_new, self.k, self.v, block_table, seq_lens, cu_new, self.k_scale, self.v_scale, stream)
 
-    def decode(self, q, block_table, seq_lens, scale: float, window: int = 0):
-        """Returns (o, lse)."""
+    def decode(self, q, block_table, seq_lens, scale: float, window: int = 0, stream=None):
+        """Returns (o, lse), as on ``stream`` (its memory is that stream's)."""
         B, Hq, d = q.shape
-        o = torch.empty_like(q)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        ws = torch.empty(fa_decode_workspace_bytes(B, Hq, self.k.shape[1], d), dtype=torch.uint8, device=q.device)
-        fa_decode(q, self.k, self.v, block_table, seq_lens, o, lse, scale, ws, self.k_scale, self.v_scale, window)
+        with torch.cuda.stream(stream) if stream is not None else _AS_IT_IS:
+            o = torch.empty_like(q)
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+            ws = torch.empty(fa_decode_workspace_bytes(B, Hq, self.k.shape[1], d), dtype=torch.uint8, device=q.device)
+            fa_decode(q, self.k, self.v, block_table, seq_lens, o, lse, scale, ws, self.k_scale, self.v_scale, window, stream)
         return o, lse
 
-    def gather(self, block_table, seq_lens, N: int, rep: int = 1):
-        """Returns (k, v), each [B, H * rep, N, d] bf16."""
+    def gather(self, block_table, seq_lens, N: int, rep: int = 1, stream=None):
+        """Returns (k, v), each [B, H * rep, N, d] bf16, as on ``stream``."""
         _, H, _, d = self.k.shape
-        k, v = (torch.empty((block_table.shape[0], H * rep, N, d), dtype=torch.bfloat16, device=self.k.device)
-                for _ in range(2))
-        fa_cache_gather(self.k, self.v, block_table, seq_lens, k, v, self.k_scale, self.v_scale)
+        with torch.cuda.stream(stream) if stream is not None else _AS_IT_IS:
+            k, v = (torch.empty((block_table.shape[0], H * rep, N, d), dtype=torch.bfloat16, device=self.k.device)
+                    for _ in range(2))
+            fa_cache_gather(self.k, self.v, block_table, seq_lens, k, v, self.k_scale, self.v_scale, stream)
         return k, v
