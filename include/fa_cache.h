@@ -24,7 +24,12 @@
  * Limits: d in {64, 128}; page_size 16, 32, 64 or a multiple of 128; k and v
  * 16-byte aligned with strides that are multiples of 16 bytes and at least one
  * row apart; B, H, num_pages, max_pages >= 1; max_pages * page_size < 2^31.
- * The cache itself may be of any size (offsets are 64-bit).
+ * The cache itself may be of any size (offsets are 64-bit).  A call's work is counted in
+ * 31 bits: fa_cache_append takes 2 * T * H < 2^31, fa_cache_gather the elements that its
+ * outputs may have, and fa_decode 6 * B * H * blocks * tiles < 2^31, with blocks = 1 for
+ * up to 32 query heads per cache head (one more for every 32 beyond) and tiles = max_pages *
+ * page_size / 128, rounded up: the table's capacity counts, whatever the lengths are.
+ * Beyond these: FA_ERR_UNSUPPORTED.
  *
  * block_table is [B][max_pages] int32 with rows block_table_stride ints apart;
  * only the entries that a sequence's length reaches are read.  seq_lens is [B]

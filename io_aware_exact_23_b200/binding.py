@@ -2,7 +2,7 @@
 
 Every function here checks tensor dtypes/shapes/devices, turns torch tensors
 into raw device pointers and the current CUDA stream into a handle, and calls
-the C entry point of the same name declared in ``include/fa.h``.  All
+the C entry point of the same name declared in ``include/fa.h`` or ``include/fa_cache.h``.  All
 arithmetic happens in the CUDA kernels.  If ``libfa.so`` is missing this module
 raises at import: there is no fallback path.
 """

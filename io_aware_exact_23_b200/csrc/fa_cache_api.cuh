@@ -193,6 +193,8 @@ int fa_cache_append(const fa_paged_cache *cache, const void *k_new, const void *
   if (T == 0) return FA_OK;
   if (!k_new || !v_new) return FA_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(cu_new)) return FA_ERR_MISALIGNED;
+  const long long total = 2ll * T * cache->H;
+  if (total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const long long *strides[2] = {k_new_stride, v_new_stride};
   const int extent[2] = {T, cache->H};
   fa::AppendParams p;
@@ -210,8 +212,6 @@ int fa_cache_append(const fa_paged_cache *cache, const void *k_new, const void *
   p.x[1] = static_cast<const uint16_t *>(v_new);
   p.cu_new = cu_new;
   p.T = T;
-  const long long total = 2ll * T * cache->H;
-  if (total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   const bool e4m3 = cache->type == FA_CACHE_E4M3;
   p.rows = rows_per_warp(total, cache->d, e4m3 ? 32 : 2048 / cache->d, ds->num_sms);
   const unsigned grid = blocks_for(total, p.rows);
