@@ -30,7 +30,7 @@
 // * e4m3: codes are multiplied as they are (kind::f8f6f4), the factor of K goes into the
 //   score, that of V into the weight.  q (8 bits, a power of two taken out of each head) is
 //   hi + lo / 32 in e4m3, exact to 2^-22 of the head's largest element.  A weight times V's factor is
-//   four e5m2 parts (decode_parts): off by 2^-15 of itself at most, or by 2^-32 of the head's
+//   four e5m2 parts (decode_parts): off by 2^-15 of itself at most, or by 2^-27 of the head's
 //   largest such product, so that many keys far below one still count (three e4m3 parts of
 //   fp16's 11 bits stopped at 2^-20 of it).
 // The columns' sums meet again in fp32.
@@ -93,9 +93,9 @@ struct DecodeCfg {
   // goes into the product is a code, weight * V's factor * a power of two per 8 heads.  A head's
   // reference is put so that its largest code is 2^kCodeLog2 (decode_references), and moves before a
   // code passes 2^(kCodeLog2 + kGrowV), or a weight 2^(kHeadLog2 + kGrow).
-  // (Room of 2^3 for the codes' growth instead of 2^5: the first tiles of most segments moved it.)
+  // (Room of 2^5 instead of 2^7: 64 x 16384 with 32 heads, d = 64, 71.4 us, 68.7 so.)
   static constexpr float kGrow = 8.f;
-  static constexpr int kCodeLog2 = 4, kGrowV = 5, kHeadLog2 = 60;
+  static constexpr int kCodeLog2 = 2, kGrowV = 7, kHeadLog2 = 80;
 
   static constexpr int kSoftmaxWarps = 4 * kGroups;
   static constexpr int kWarps = kSoftmaxWarps + 8;  // softmax, 4 epilogue, producer, issuer, Q, scales
@@ -116,9 +116,9 @@ struct DecodeCfg {
   static constexpr int kQOff = kPOff + 2 * kPBytes;
   static constexpr int kRingOff = (kQOff + 2 * kQBytes + 1023) / 1024 * 1024;
   // Behind the ring: factors, then floats xmax[2][GB][4], lpart[2][4][GB], mstat[2][GB], of e4m3
-  // vmax[2][GB][4] and refs[4][3][GB], and qscale[2][GB], vstat[2][kGroups], then barriers and words.
+  // vmax[2][GB][4], refs[4][4][GB], qscale[2][GB], vstat[2][GB] and vspan[2][kGroups][4] pairs, then barriers and words.
   static constexpr int kScBytes = E4M3 ? kScStages * 1024 : 0;
-  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + (E4M3 ? 22 * GB : 0) + 4 * kGroups;
+  static constexpr int kMiscFloats = 2 * GB * 4 + 2 * 4 * GB + 2 * GB + (E4M3 ? 28 * GB + 16 * kGroups : 0);
   static constexpr int kFixedBars = 20 + 2 * kScStages;
   static constexpr int kTailBytes = kScBytes + kMiscFloats * 4 + kFixedBars * 8 + 16 * 4;
   static constexpr int kFit = (kSmemMax - kRingOff - kTailBytes) / (kTileBytes + 16);
@@ -305,6 +305,10 @@ __device__ __forceinline__ void decode_parts(uint64_t c, uint32_t (&p)[4]) {
   p[3] = pack_e5m2(a, b);
 }
 
+// Where a tile's factors are within this of each other, the largest one and a head's largest weight stand for
+// its largest product (else that takes a second exchange between the warps).
+constexpr float kFactorSpan = 8.f;
+
 // The references of one query head of an e4m3 cache: m, its largest score (log2) so far; e, a power
 // of two that its products of weight (relative to m) and V's factor have not passed; and r = m -
 // delta, the reference of the scores, with a whole delta in [0, kHeadLog2].
@@ -312,10 +316,10 @@ __device__ __forceinline__ void decode_parts(uint64_t c, uint32_t (&p)[4]) {
 // softmax warp: 2^kCodeLog2 / the largest of their e, so that theirs is the largest code.  A head whose
 // products are smaller has its scores' reference lowered by as much (its weights raised), and so its own
 // largest code where the others' is; only below 2^-kHeadLog2 of them does it lose resolution.
-// Weights, codes and sums stay in range: a weight is at most 2^kHeadLog2 on r, and r is rounded up where
-// m is so large that it cannot hold the difference.
+// Weights, codes and sums stay in range: a weight is at most 2^kHeadLog2 on r, and r is rounded up (m with
+// it) where it cannot hold the difference.  A segment's sums leave it on m again: l * unit, exact.
 struct DecodeRefs {
-  float m, r, e;
+  float m, r, e, unit;  // unit: 2^-delta
 };
 // Products as powers of two, within [2^-116, 2^126].
 __device__ __forceinline__ uint32_t decode_power(float x) {
@@ -326,22 +330,14 @@ __device__ __forceinline__ DecodeRefs decode_references(float m, float product, 
   const uint32_t mine = decode_power(product), most = __reduce_max_sync(0xffffffffu, mine);
   code = ((254u + C::kCodeLog2) << 23) - most;  // 2^kCodeLog2 / most
   const uint32_t delta = min((most - mine) >> 23, static_cast<uint32_t>(C::kHeadLog2));
-  return {m, __fadd_ru(m, -static_cast<float>(delta)), __uint_as_float(most - (delta << 23))};
+  const float less = static_cast<float>(delta), r = __fadd_ru(m, -less);
+  return {r + less, r, __uint_as_float(most - (delta << 23)), __uint_as_float((127u - delta) << 23)};
 }
 
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// ln(2^m l): l's exponent goes to m first, whose rounding is the result's; with log2(l) alone a large
-// exponent would cost the result's last bits.
-__device__ __forceinline__ float decode_lse(float m, float l) {
-  const uint32_t b = __float_as_uint(l);
-  if (b - 0x00800000u >= 0x7f000000u) return (m + log2f(l)) * 0.69314718055994531f;  // 0, NaN, infinity
-  return ((m + static_cast<float>(static_cast<int>(b >> 23) - 127)) + log2f(__uint_as_float((b & 0x7fffffu) | 0x3f800000u))) *
-         0.69314718055994531f;
 }
 
 // Barrier `id` over `n` threads that also returns whether any of them passed true.
@@ -385,6 +381,27 @@ __device__ __forceinline__ void reduce_columns(float (&v)[N], F f) {
     bit >>= 1;
   }
   for (; bit >= 1; bit >>= 1) v[0] = f(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+}
+
+// The columns' largest values, in the lanes that reduce_columns leaves them in (NaN aside).  Few columns
+// go through the integer reduction, on bits ordered as the numbers are (256 short e4m3 sequences of one
+// head, d = 64, 62.5 us with the shuffles, 57.5 so); of 8, the shuffles are as fast.
+template <int N>
+__device__ __forceinline__ float max_columns(float (&v)[N]) {
+  if constexpr (N > 4) {
+    reduce_columns<N>(v, [](float a, float b) { return fmaxf(a, b); });
+    return v[0];
+  } else {
+    const int mine = (threadIdx.x & 31) / (32 / N);
+    int best = 0;
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+      const int b = __float_as_int(fmaxf(v[g], -INFINITY));
+      const int r = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+      best = mine == g ? r : best;
+    }
+    return __int_as_float(best ^ ((best >> 31) & 0x7fffffff));
+  }
 }
 
 // `total` units of cost dealt out to `nc` CTAs, the first of them one more where it does not
@@ -528,6 +545,32 @@ struct DecodePages {
   }
 };
 
+// The tile's largest products of weight (relative to mx, of head lane / (32 / H)) and factor, over a
+// group's four warps: head lane / (32 / H)'s.  Out of line: rare, and instruction fetch is scarce (256 short
+// e4m3 sequences of one head, d = 64: 57.0 us, 58.1 in line).
+template <int N>
+struct DecodeScores {
+  uint64_t v2[N];
+};
+template <int H>
+__device__ __noinline__ float decode_products(DecodeScores<H / 2> s, float mx, float fv, float *vr, uint32_t bar) {
+  constexpr int kSpan = 32 / H;
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3;
+  float t[H];
+#pragma unroll
+  for (int g = 0; g < H / 2; ++g) {
+    float a, b;
+    f2unpack(s.v2[g], a, b);
+    t[2 * g] = fmaxf(ex2(a - __shfl_sync(0xffffffffu, mx, 2 * g * kSpan)), 0x1p-120f) * fabsf(fv);
+    t[2 * g + 1] = fmaxf(ex2(b - __shfl_sync(0xffffffffu, mx, (2 * g + 1) * kSpan)), 0x1p-120f) * fabsf(fv);
+  }
+  const float most = max_columns<H>(t);
+  if (lane % kSpan == 0) vr[lane / kSpan * 4 + w4] = most;
+  bar_any(bar, 128, false);
+  const float4 t4 = *reinterpret_cast<const float4 *>(vr + lane / kSpan * 4);
+  return fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w));
+}
+
 // Note an item that begins in this CTA for the join kernel: its parts up to the CTA that holds
 // its last unit of cost (0: it is whole).  Out of line: once an item at most.
 __device__ __noinline__ void decode_note(const DecodeParams &p, int b, int h, int blk, int row, int last, int total, int nc) {
@@ -566,10 +609,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
   float *lpart = xmax + 2 * GB * 4;                               // [2][4][GB]
   float *mstat = lpart + 2 * 4 * GB;                              // [2][GB]
   float *vmaxw = mstat + 2 * GB;                                  // e4m3: [2][GB][4], read as float4 like xmax
-  float *refs = vmaxw + 8 * GB;                                   // e4m3: [4][3][GB], a warp's own
-  float *qscale = E4M3 ? refs + 12 * GB : vmaxw;                  // e4m3: [2][GB]
-  float *vstat = E4M3 ? qscale + 2 * GB : vmaxw;                  // e4m3: [2][kGroups]
-  static_assert(C::kMiscOff % 16 == 0 && (18 * GB) % 4 == 0, "xmax and vmaxw on 16 bytes");
+  float *refs = vmaxw + 8 * GB;                                   // e4m3: [4][4][GB], a warp's own
+  float *qscale = E4M3 ? refs + 16 * GB : vmaxw;                  // e4m3: [2][GB]
+  float *vstat = E4M3 ? qscale + 2 * GB : vmaxw;                  // e4m3: [2][GB]
+  float2 *vspan = reinterpret_cast<float2 *>(vstat + 2 * GB);       // e4m3: [2][kGroups][4]
+  static_assert(C::kMiscOff % 16 == 0 && (18 * GB) % 4 == 0 && C::kMiscFloats % 4 == 0, "xmax and vmaxw on 16 bytes");
   uint8_t *ring = smem + C::kRingOff;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
@@ -1000,7 +1044,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
     float *xm = xmax + kH * grp * 4;
     uint64_t nm2[kPairs], l2[kPairs];           // minus the reference, and this key's sum of weights
     float code = 1.f;  // e4m3: of the group's heads (decode_references)
-    float *ref = refs + 3 * w4 * GB + kH * grp + lane / kSpan;  // of head lane / kSpan: m, r and e, GB apart
+    float *ref = refs + 4 * w4 * GB + kH * grp + lane / kSpan;  // of head lane / kSpan: m, r, e and unit, GB apart
     bool bad = false, stop = false;
     int n = 0, nred = 0, sv = 1;      // tiles, reductions, ring slot of the tile's V
     uint32_t vph = 0;
@@ -1087,7 +1131,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           float top = x[0];
 #pragma unroll
           for (int g = 1; g < kH; ++g) top = fmaxf(top, x[g]);
-          grow = top > room;
+          grow = top >= room;  // (room is -inf where factor * code overflows, and top where all weights are 0)
           grow = bar_any(bar_a, 128, grow || bad);
         }
         if (grow) {
@@ -1096,8 +1140,18 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           float v[kH];
 #pragma unroll
           for (int g = 0; g < kPairs; ++g) f2unpack(v2[g], v[2 * g], v[2 * g + 1]);
-          reduce_columns<kH>(v, [](float a, float b) { return fmaxf(a, b); });
+          if constexpr (E4M3)
+            v[0] = max_columns<kH>(v);
+          else
+            reduce_columns<kH>(v, [](float a, float b) { return fmaxf(a, b); });
           if (lane % kSpan == 0) xr[lane / kSpan * 4 + w4] = v[0];
+          float2 *span = vspan + ((nred & 1) * C::kGroups + grp) * 4;
+          if constexpr (E4M3) {
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(fv)));
+            const bool seen = pos0 + key >= wk.first && pos0 + key < wk.len;
+            const uint32_t least = __reduce_min_sync(0xffffffffu, seen ? __float_as_uint(fabsf(fv)) : 0x7f800000u);
+            if (lane == 0) span[w4] = make_float2(__uint_as_float(most), __uint_as_float(least));
+          }
           if (bar_any(bar_b, 128, bad)) {
             stop = true;
             break;
@@ -1122,36 +1176,51 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
               if (i > 0) l2[g] = mul2(l2[g], f2pack(alpha[2 * g], alpha[2 * g + 1]));
             }
           } else {
-            // The tile's largest products relative to the new maxima: a value row counts with the weight
-            // it has, and one much larger than the others that is hardly seen leaves their resolution alone.
-            DecodeRefs old = {mc, 0.f, 0.f};
-            if (i > 0) old = {ref[0], ref[GB], ref[2 * GB]};
-            const float mx = fmaxf(mc, old.m);
-            float t[kH];
-#pragma unroll
-            for (int g = 0; g < kPairs; ++g) {
-              float a, b;
-              f2unpack(v2[g], a, b);
-              t[2 * g] = ex2(a - __shfl_sync(0xffffffffu, mx, 2 * g * kSpan)) * fabsf(fv);
-              t[2 * g + 1] = ex2(b - __shfl_sync(0xffffffffu, mx, (2 * g + 1) * kSpan)) * fabsf(fv);
-            }
-            reduce_columns<kH>(t, [](float a, float b) { return fmaxf(a, b); });
-            float *vr = vmaxw + (kH * grp + (nred & 1) * GB) * 4;
-            if (lane % kSpan == 0) vr[lane / kSpan * 4 + w4] = t[0];
-            bar_any(bar_b, 128, false);
-            const float4 t4 = *reinterpret_cast<const float4 *>(vr + lane / kSpan * 4);
+            // Rows of Q without a head (next to ones that have) have no say and no weight.
+            const int live = p.G - wk.blk * GB - kH * grp;
+            const bool none = live > 0 && lane / kSpan >= live;
+            const float4 s0 = reinterpret_cast<const float4 *>(span)[0], s1 = reinterpret_cast<const float4 *>(span)[1];
+            const float most = fmaxf(fmaxf(s0.x, s0.z), fmaxf(s1.x, s1.z)), least = fminf(fminf(s0.y, s0.w), fminf(s1.y, s1.w));
+            DecodeRefs now;
             uint32_t next;
-            const DecodeRefs now = decode_references<C>(
-                mx, fmaxf(fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w)), old.e * ex2(old.m - mx)), next);
-            // O goes by the codes, l by the weights.
-            const float up = static_cast<float>(static_cast<int>(next >> 23) - static_cast<int>(__float_as_uint(code) >> 23));
-            const float of_l = ex2(old.r - now.r), of_o = ex2((old.r - now.r) + up);
+            float of_l = 1.f, of_o = 1.f;  // what l and O are multiplied by
+            const bool alike = most <= kFactorSpan * least;
+            if (i == 0 && alike) {
+              // Every head has a weight of 1 in the tile: the largest factor will do for all their products.
+              const uint32_t e = decode_power(most);
+              next = ((254u + C::kCodeLog2) << 23) - e;
+              now = {mc, mc, __uint_as_float(e), 1.f};
+            } else {
+              DecodeRefs old = {mc, 0.f, 0.f, 0.f};
+              if (i > 0) old = {ref[0], ref[GB], ref[2 * GB], 0.f};
+              const float mx = fmaxf(mc, old.m);
+              // The tile's largest product relative to the new maximum.  (No factor, seen or not, above 2^120
+              // times it: factor * code stays finite.)
+              float product;
+              if (alike) {
+                product = fmaxf(ex2(mc - mx), 0x1p-120f) * most;  // its own largest weight times any factor
+              } else {
+                // A value row counts with the weight it has: one much larger than the others that is hardly
+                // seen leaves their resolution alone.
+                DecodeScores<kPairs> scores;
+#pragma unroll
+                for (int g = 0; g < kPairs; ++g) scores.v2[g] = v2[g];
+                product = decode_products<kH>(scores, mx, fv, vmaxw + (kH * grp + (nred & 1) * GB) * 4, bar_b);
+              }
+              now = decode_references<C>(mx, none ? 0.f : fmaxf(product, old.e * ex2(old.m - mx)), next);
+              // O goes by the codes, l by the weights.
+              const float up = static_cast<float>(static_cast<int>(next >> 23) - static_cast<int>(__float_as_uint(code) >> 23));
+              of_l = ex2(old.r - now.r);
+              of_o = ex2((old.r - now.r) + up);
+            }
+            if (none) now.r = INFINITY;
             code = __uint_as_float(next);
             __syncwarp();
             if (lane % kSpan == 0) {
               ref[0] = now.m;
               ref[GB] = now.r;
               ref[2 * GB] = now.e;
+              ref[3 * GB] = now.unit;
             }
             __syncwarp();
 #pragma unroll
@@ -1261,12 +1330,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         f2unpack(nm2[g], m[2 * g], m[2 * g + 1]);
       }
       reduce_columns<kH>(l, [](float a, float b) { return a + b; });
-      if (lane % kSpan == 0) lpart[(ob * 4 + w4) * GB + kH * grp + lane / kSpan] = l[0];
-      if (w4 == 0 && lane == 0) {
+      if constexpr (E4M3) {
+        // On the maximum, and what a code stands for.  (Parts of a sequence have references of their
+        // own, and the join's exponentials no room for their deltas.)
+        l[0] *= ref[3 * GB];
+        if (w4 == 0 && lane % kSpan == 0) {
+          mstat[ob * GB + kH * grp + lane / kSpan] = ref[0];
+          vstat[ob * GB + kH * grp + lane / kSpan] = ref[2 * GB] * (1.f / (1 << C::kCodeLog2));
+        }
+      } else if (w4 == 0 && lane == 0) {
 #pragma unroll
         for (int g = 0; g < kH; ++g) mstat[ob * GB + kH * grp + g] = -m[g];
-        if constexpr (E4M3) vstat[ob * C::kGroups + grp] = __uint_as_float((254u << 23) - __float_as_uint(code));  // 1 / code
       }
+      if (lane % kSpan == 0) lpart[(ob * 4 + w4) * GB + kH * grp + lane / kSpan] = l[0];
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bar_stat[ob]);
@@ -1325,12 +1401,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
         const float lt = (lp[0] + lp[GB]) + (lp[2 * GB] + lp[3 * GB]);
         const float mh = mstat[ob * GB + gc + (lane & (kH - 1))];
         const float mul = whole ? __fdividef(1.f, lt) : 1.f;
-        const float unit = E4M3 ? vstat[ob * C::kGroups + gc / kH] : 1.f;  // of a code
+        float unit[kH];  // e4m3: what a code stands for
+#pragma unroll
+        for (int e = 0; e < kH; ++e) unit[e] = E4M3 ? vstat[ob * GB + gc + e] : 1.f;
         if ((warp & 3) == 0 && lane < kH && gc + lane < ng) {
           if (!whole)
             p.part_ml[slot * GB + gc + lane] = make_float2(mh, lt);
           else if (p.lse)
-            p.lse[row0 + gc + lane] = decode_lse(mh, lt);
+            p.lse[row0 + gc + lane] = (mh + log2f(lt)) * 0.69314718055994531f;
         }
         tmem_wait_ld();
         uint16_t *po = p.o + (row0 + gc) * D + f;
@@ -1343,7 +1421,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           else if (fabsf(v) != INFINITY)  // an infinite value: the low part's product with it may be NaN
             v += __uint_as_float(o[1][e]);
           v *= __shfl_sync(0xffffffffu, mul, e);
-          if constexpr (E4M3) v *= unit;  // apart: their product may lie below fp32's range
+          if constexpr (E4M3) v *= unit[e];  // apart: their product may lie below fp32's range
           if (gc + e < ng) {
             if (whole)
               po[e * D] = static_cast<uint16_t>(pack_bf16(v, 0.f));
@@ -1448,7 +1526,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_decode_join_kernel(const __gr
   const float inv = __fdividef(1.f, L);
   *reinterpret_cast<uint2 *>(p.o + out * D + 4 * col) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (col == 0 && p.lse) p.lse[out] = decode_lse(M, L);
+  if (col == 0 && p.lse) p.lse[out] = (M + log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace fa

@@ -18,12 +18,12 @@ def decode_tight(c: Cache, q, scale, window=0, b=0, n=None):
       is taken off, 2^-22 |s| + 2^-24 |max s|; for e4m3 keys an element of q is off by at most
       2^-22 of the largest of its own head;
     * in e4m3 a score is taken relative to a reference that may lie below the head's largest one, by as
-      many powers of two as V's visible factors differ (60 at most): 2^-24 of those;
+      many powers of two as V's visible factors differ (80 at most): 2^-24 of those;
     * the exponential adds 2^-21.  A key's weight is then off by its own score's error e_j
       and by the normaliser's, E = log sum_j p_j exp(e_j);
     * a weight (e4m3: times V's factor) goes into the product with an error of at most 2^-15
       of itself (bf16 hi + lo: 2^-16; e4m3: fp16 and an e5m2 remainder), or 2^-29 units where the largest
-      product of weight and factor has a code between 2^3 and 2^4, times V's 448;
+      product of weight and factor has a code of at least 2^-2, times V's 448;
     * the product adds 16 or 32 keys at a time to an fp32 accumulator that may truncate, and
       within those aligns them to the largest: 2^-22 of sum p|v| for each time.
     """
@@ -42,7 +42,7 @@ def decode_tight(c: Cache, q, scale, window=0, b=0, n=None):
         e += 2.0**-22 * scale * qb.abs().amax(-1, keepdim=True) * K.abs().sum(-1)[:, None]
         page, off = c.where(b, torch.arange(lo, n, device=DEV))
         f = c.vs[page, :, off].double().abs().t()  # [H, m]
-        apart = (torch.log2(f.amax(1) / f.amin(1)) + 2).clamp_max(60)
+        apart = (torch.log2(f.amax(1) / f.amin(1)) + 2).clamp_max(80)
         e += 2.0**-24 * apart[:, None, None]
     e += 2.0**-22 * s.abs() + 2.0**-24 * s.abs().amax(-1, keepdim=True) + 2.0**-21
     E = torch.log((p * torch.exp(e)).sum(-1, keepdim=True))
@@ -50,7 +50,7 @@ def decode_tight(c: Cache, q, scale, window=0, b=0, n=None):
     o = torch.matmul(p, V)
     do = torch.matmul(p * (torch.expm1(e + E) + (2.0**-15 if c.e4m3 else 2.0**-16) + sums), V.abs())
     if c.e4m3:
-        do += m * 2.0**-32 * 448 * (p * f[:, None]).amax(-1, keepdim=True)
+        do += m * 2.0**-27 * 448 * (p * f[:, None]).amax(-1, keepdim=True)
     dl = E + sums + 2.0**-22 * z.abs()
     return o.reshape(Hq, d), z.reshape(Hq), do.reshape(Hq, d), dl.reshape(Hq)
 

@@ -104,6 +104,69 @@ def test_scores_that_climb_while_values_shrink(d, sign):
     check_tight(o[0], L[0], ref)
 
 
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 12, 16, 31])
+@pytest.mark.parametrize("score", [-80.0, -200.0])
+@pytest.mark.parametrize("value", [1e30, 3e38])
+def test_a_value_row_at_the_end_of_the_type(value, score, G):
+    """Hardly seen, or not at all: it leaves every head's other values alone.  First in its segment, last and between."""
+    n, d = 700, 64
+    for at in (0, 300, 699):
+        c = Cache([n], 1, d, 16, True, seed=30, fill=False)
+        s = rows(n, 1, 1, 31).flatten()
+        s[at] = score
+        q = aimed(c, s, G)
+        v = rows(n, 1, d, 32, mean=0.5)
+        v[at] = value
+        c.put(c.v, c.vs, 0, torch.arange(n, device=DEV), v.to(torch.bfloat16))
+        o, L = run(fa, c, q[None])
+        check_tight(o[0], L[0], decode_tight(c, q, 1.0), f"at {at}")
+
+
+@pytest.mark.parametrize("G", [2, 3, 8, 16])
+@pytest.mark.parametrize("apart", [2.0**30, 2.0**50, 2.0**70])
+@pytest.mark.parametrize("n", [200, 5000])
+def test_heads_that_see_values_of_different_size(n, apart, G):
+    """Even heads attend to keys with small values, odd ones to keys with values `apart` times
+    those; each is as exact as if the other was not there."""
+    d = 64
+    c = Cache([n], 1, d, 16, True, seed=33, fill=False)
+    at = torch.arange(n, device=DEV)
+    odd = at % 2 == 1
+    r = 0.5 * rows(n, 1, d, 34)
+    r[:, 0, 0], r[:, 0, 1] = torch.where(odd, -60.0, 0.0), torch.where(odd, 0.0, -60.0)
+    c.put(c.k, c.ks, 0, at, r.to(torch.bfloat16))
+    v = rows(n, 1, d, 35, mean=1.0) * torch.where(odd, apart**0.5, apart**-0.5)[:, None, None]
+    c.put(c.v, c.vs, 0, at, v.to(torch.bfloat16))
+    g = torch.Generator(device="cpu").manual_seed(36)
+    q = (0.1 * torch.randn(G, d, generator=g)).to(torch.bfloat16).to(DEV)
+    q[:, 0], q[:, 1] = 0, 0
+    q[0::2, 0], q[1::2, 1] = 2, 2
+    o, L = run(fa, c, q[None])
+    check_tight(o[0], L[0], decode_tight(c, q, 1.0))
+
+
+def test_parts_whose_values_differ():
+    """A split sequence whose first half has scores 34 nats below the second's and values 2^70 times
+    as large, next to a head that sees both alike: the parts are joined on their own maxima."""
+    n, d = 40000, 64
+    c = Cache([n], 1, d, 64, True, seed=37, fill=False)
+    at = torch.arange(n, device=DEV)
+    first = at < n // 2
+    r = torch.zeros(n, 1, d, device=DEV)
+    r[:, 0, 0] = torch.where(first, -34.0, 0.0)
+    r[::2, 0, 1] = -80.0  # seen by the second head alone
+    c.put(c.k, c.ks, 0, at, r.to(torch.bfloat16))
+    v = rows(n, 1, d, 38, mean=1.0) * torch.where(first, 2.0**35, 2.0**-35)[:, None, None]
+    v[::2] *= 2.0**40
+    c.put(c.v, c.vs, 0, at, v.to(torch.bfloat16))
+    q = torch.zeros(4, d, dtype=torch.bfloat16, device=DEV)
+    q[:, 0] = 1
+    q[:3, 1] = 1
+    q[3, 1] = -1
+    o, L = run(fa, c, q[None])
+    check_tight(o[0], L[0], decode_tight(c, q, 1.0))
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("G", [1, 2, 4, 8, 16, 32])
 @pytest.mark.parametrize("d", [64, 128])
