@@ -182,6 +182,33 @@ def test_ordinary_rows(d, G, e4m3):
             check_tight(o[b], L[b], decode_tight(c, q[b], 0.3, b=b), f"sequence {b}")
 
 
+@pytest.mark.parametrize("G", [1, 3, 8, 32])
+@pytest.mark.parametrize("alike", [True, False])
+@pytest.mark.parametrize("score", [1e5, 3e8, 1e30, -1e5, -3e8, -1e30])
+def test_scores_far_from_zero(score, alike, G):
+    """Equal scores so large that a reference a few powers of two below them is lost in their rounding,
+    and ones ten times lower before and after them."""
+    n, d = 500, 64
+    c = Cache([n], 1, d, 16, True, seed=40, fill=False)
+    at = torch.arange(n, device=DEV)
+    high = (at >= 150) & (at < 400)
+    lower = score / 10 if score > 0 else score * 10
+    q = aimed(c, torch.where(high, score, lower), G)
+    v = rows(n, 1, d, 41, mean=1.0)
+    if not alike:
+        v = v * torch.exp2((at % 23 - 11).float())[:, None, None]
+    c.put(c.v, c.vs, 0, at, v.to(torch.bfloat16))
+    o, L = run(fa, c, q[None])
+    K, V = c.rows("k", 0, n)[0, :, 0], c.rows("v", 0, n)[0]
+    page, off = c.where(0, at)
+    ref, mag = V[high].mean(0), V[high].abs().mean(0)
+    # Equal weights: their rounding (2^-15, or 2^-27 of the largest product's 448), sums and o's own.
+    err = (2.0**-15 + (n / 16 + 8) * 2.0**-22) * mag + 2.0**-27 * 448 * c.vs[page, :, off].max().double()
+    assert ((o[0].double() - ref).abs() <= 2.0**-8 * (ref.abs() + err) + err).all()
+    want = float(K[high][0]) + float(torch.log(high.sum().double()))
+    assert ((L[0].double() - want).abs() <= 2.0**-22 * abs(want)).all()
+
+
 # ----------------------------------------------------------------- queries
 @pytest.mark.parametrize("G", [2, 4, 8, 24])
 @pytest.mark.parametrize("d", [64, 128])
