@@ -17,9 +17,10 @@
 // (lengths, share, page ids), 3 for a tile, 2.4 for the join.
 //
 // Work split.  A tile is 128 positions of one (sequence, cache head, block of at most GB
-// query heads).  All tiles, in that order, are dealt out evenly: CTA c of nc takes tiles
-// [T c / nc, T (c + 1) / nc), so SMs finish together whatever the lengths, and a sequence
-// is split over the cache's length exactly where a CTA's share ends.  A CTA walks its
+// query heads), and an item such a triple's tiles.  All tiles, in that order, are dealt out by their
+// cost, an item's start and end included (DecodeCfg, DecodeSplit): CTA c of nc takes those that
+// begin in its nc-th part of the total, so SMs finish together whatever the lengths, and a
+// sequence is split over the cache's length exactly where a CTA's share ends.  A CTA walks its
 // share as segments (runs of one item's tiles); an item held by one CTA is written out
 // whole, the others leave (m, l, O) per segment in the workspace and fa_decode_join_kernel
 // adds them up in a fixed order.
@@ -37,7 +38,7 @@
 //
 // Softmax warps.  Four warps own the 128 keys of a tile for 8 query heads, GB / 8 such
 // groups per CTA.  P is the MN-major operand: a key's weights are adjacent bytes, so a
-// thread stores its 8 heads with two or three vector stores.  (With P K-major, one 2-byte
+// thread stores its 8 heads with one vector store a part.  (With P K-major, one 2-byte
 // or 1-byte store per head and part, and all GB heads in one thread, a tile took 3000 to
 // 4000 cycles in e4m3; its share of the memory's rate allows 1430 at d = 128.)
 #pragma once
