@@ -1070,7 +1070,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           fv = __fmaf_rn(sc[128 + key], 0.f, sc[128 + key]);
         }
         // How far a weight (log2) may go before the references move.  e4m3: the code's limit, or the weight's.
-        const float room = E4M3 ? fminf(C::kCodeLog2 + C::kGrowV - lg2(fabsf(fv * code)), C::kHeadLog2 + C::kGrow) : C::kGrow;
+        float room = E4M3 ? fminf(C::kCodeLog2 + C::kGrowV - lg2(fabsf(fv * code)), C::kHeadLog2 + C::kGrow) : C::kGrow;
         bad |= !decode_wait(ctx, &bar_s[buf], (n >> 1) & 1, kTagDS);
         __syncwarp();
         tc_fence_after();
@@ -1105,6 +1105,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
           const bool valid = pos >= wk.first && pos < wk.len;
           if (!valid) {
             fv = 0.f;
+            room = INFINITY;  // what the row has for a factor must not move anything
 #pragma unroll
             for (int g = 0; g < kPairs; ++g) v2[g] = f2pack(-INFINITY, -INFINITY);
           }

@@ -209,6 +209,34 @@ def test_scores_far_from_zero(score, alike, G):
     assert ((L[0].double() - want).abs() <= 2.0**-22 * abs(want)).all()
 
 
+@pytest.mark.parametrize("G", [1, 4, 8, 20])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_are_not_seen_leave_every_bit_alone(d, G):
+    """Behind a sequence's end, and before its window, the pages' rows may hold anything: factors at the
+    end of the type must not move a reference."""
+    lens = [200, 129, 300, 17] * 100  # enough for segments of several tiles
+    B = len(lens)
+    for window in (0, 150):
+        c = Cache(lens, 1, d, 64, True, seed=50)
+        g = torch.Generator(device="cpu").manual_seed(51)
+        q = (1.5 * torch.randn(B, G, d, generator=g)).to(torch.bfloat16).to(DEV)
+        seen = torch.zeros_like(c.ks, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            page, off = c.where(b, torch.arange(max(0, n - window) if window else 0, n, device=DEV))
+            seen[page, :, off] = True
+        want = None
+        for other in (1e-3, 3.4e38, float("inf"), float("nan"), 0.0):
+            for f, codes in ((c.ks, c.k), (c.vs, c.v)):
+                f[~seen] = other
+                codes[~seen] = 0x7E  # 448
+            o, L = run(fa, c, q, scale=0.3, window=window)
+            if want is None:
+                want = o, L
+                for b in range(8):
+                    check_tight(o[b], L[b], decode_tight(c, q[b], 0.3, window, b=b), f"sequence {b}")
+            assert torch.equal(o, want[0]) and torch.equal(L, want[1]), f"factors of {other}"
+
+
 # ----------------------------------------------------------------- queries
 @pytest.mark.parametrize("G", [2, 4, 8, 24])
 @pytest.mark.parametrize("d", [64, 128])
