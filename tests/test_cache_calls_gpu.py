@@ -4,6 +4,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+from cache_bounds import check_tight, decode_tight
 from cache_helpers import DEV, Cache, check_decode, decode_exact
 from io_aware_exact_23_b200 import binding as fa
 
@@ -69,3 +70,63 @@ def test_wrapper_on_a_stream(e4m3):
             want = ref.rows(nm, b, n).repeat_interleave(2, 0)
             assert ((t[b, :, :n].double() - want).abs() <= (2.0**-8 + 2.0**-23) * want.abs()).all()
     assert (k[1] == 0).all() and (v[2, :, 33:] == 0).all()
+
+
+# ------------------------------------------------ calls that begin while the last one ends
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_decode_s_output_is_the_next_one_s_query(e4m3):
+    """No kernel in between: each call may start while the one that writes its q still runs."""
+    c = [Cache([700, 0, 90, 33], 2, 128, 16, e4m3, layout, seed=i) for i, layout in enumerate(("hnd", "nhd"))]
+    start = torch.randn(4, 8, 128, device=DEV).to(torch.bfloat16)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(4, 8, 2, 128), dtype=torch.uint8, device=DEV)
+
+    def chain(wait):
+        x, out = start.clone(), []
+        for t in range(24):
+            y = torch.empty_like(x)
+            if wait:
+                torch.cuda.synchronize()
+            cc = c[t % 2]
+            fa.fa_decode(x, cc.k, cc.v, o=y, lse=None, scale=0.3, workspace=ws, **cc.args)
+            out.append(y)
+            x = y
+        return out
+
+    slow = chain(True)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = chain(False)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status() == 0
+        for t, (a, b) in enumerate(zip(got, slow)):
+            assert torch.equal(a, b), f"step {t}"
+
+
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "padded"])
+@pytest.mark.parametrize("H", [1, 3])
+def test_decodes_see_each_append_s_factors(H, layout):
+    """Steps of append and decode in a row over the same lines of factors, tokens adjacent or not:
+    what a decode has read of them before is not what the next one uses."""
+    steps, B, d = 50, 3, 64
+    c = Cache([steps + 40] * B, H, d, 16, True, layout, seed=7)
+    c.lens.copy_(torch.tensor([30, 1, 17], dtype=torch.int32))
+    q = torch.randn(B, 4 * H, d, device=DEV).to(torch.bfloat16)
+    ws = torch.empty(fa.fa_decode_workspace_bytes(B, 4 * H, H, d), dtype=torch.uint8, device=DEV)
+    # Sizes that change from step to step: a factor of the step before would show.
+    size = torch.exp2(torch.arange(steps, device=DEV) * 5 % 17 - 8.0)[:, None, None, None, None]
+    new = (torch.randn(steps, 2, B, H, d, device=DEV) * size).to(torch.bfloat16)
+    lens = [c.lens + t + 1 for t in range(steps)]
+    out = []
+    torch.cuda.synchronize()
+    for t in range(steps):
+        args = dict(c.args, seq_lens=lens[t])
+        fa.fa_cache_append(new[t, 0], new[t, 1], c.k, c.v, **args)
+        o, L = torch.empty_like(q), torch.empty(B, 4 * H, device=DEV)
+        fa.fa_decode(q, c.k, c.v, o=o, lse=L, scale=0.02, workspace=ws, **args)
+        out.append((o, L))
+    assert fa.fa_device_status() == 0
+    for t in range(steps):
+        check_decode(*out[t], decode_exact(c, q, 0.02, lens=lens[t].tolist()), f"step {t}")
+        for b in range(B):
+            ref = decode_tight(c, q[b], 0.02, b=b, n=int(lens[t][b]))
+            check_tight(out[t][0][b], out[t][1][b], ref, f"step {t}, sequence {b}")
