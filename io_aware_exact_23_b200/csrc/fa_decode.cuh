@@ -1225,13 +1225,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, E4M3, GB>::kThreads, DecodeCfg<D,
               ref[3 * GB] = now.unit;
             }
             __syncwarp();
+            auto head = [&](float v, int g) { return __shfl_sync(0xffffffffu, v, g * kSpan); };
 #pragma unroll
             for (int g = 0; g < kPairs; ++g) {
-              nm2[g] = f2pack(-__shfl_sync(0xffffffffu, now.r, 2 * g * kSpan), -__shfl_sync(0xffffffffu, now.r, (2 * g + 1) * kSpan));
+              nm2[g] = f2pack(-head(now.r, 2 * g), -head(now.r, 2 * g + 1));
               if (i > 0) {
-                alpha[2 * g] = __shfl_sync(0xffffffffu, of_o, 2 * g * kSpan);
-                alpha[2 * g + 1] = __shfl_sync(0xffffffffu, of_o, (2 * g + 1) * kSpan);
-                l2[g] = mul2(l2[g], f2pack(__shfl_sync(0xffffffffu, of_l, 2 * g * kSpan), __shfl_sync(0xffffffffu, of_l, (2 * g + 1) * kSpan)));
+                alpha[2 * g] = head(of_o, 2 * g);
+                alpha[2 * g + 1] = head(of_o, 2 * g + 1);
+                l2[g] = mul2(l2[g], f2pack(head(of_l, 2 * g), head(of_l, 2 * g + 1)));
               }
             }
           }
