@@ -126,13 +126,14 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int H, int d);
  * log) or NULL.  Hq is a multiple of H.  o may be q itself (a row of q is last read
  * before its row of o is written), and overlaps nothing else.  A sequence of length 0
  * gets o = 0 and lse = -inf.  Scores, statistics and sums are fp32; o is rounded once, to bf16.
- * What the products round before that: bf16 weights to 16 bits; with FA_CACHE_E4M3 an element of
- * q to within 2^-22 of the largest of its row, and a weight times V's factor to within 2^-15 of itself
- * or 2^-27 of the head's largest such product (of 2^-80 of the largest among the heads that share the
- * cache head, or 2^-120 of V's largest visible factor, where that is more).  A visible row of such a
- * cache whose factor is not finite makes its heads' o NaN.  The products' sums are the tensor
- * core's, which drop what lies below fp32's last place: a part of 2^-23 at most for every 16
- * (bf16) or 32 (e4m3) positions that one block takes of a sequence.
+ * What the products round before that: weights below 2^-126 of the largest are 0, other bf16
+ * weights have 16 bits; with FA_CACHE_E4M3 an element of q is held to within 2^-22 of the largest of
+ * its row, and a weight times V's factor to within 2^-15 of itself or 2^-27 of the head's largest such
+ * product (of 2^-80 of the largest among the heads that share the cache head, or 2^-120 of V's
+ * largest visible factor, where that is more).  A visible row of such a cache whose factor is not
+ * finite makes its heads' o NaN.  The products' sums are the tensor core's, which drop what lies
+ * below fp32's last place: a part of 2^-23 at most for every 16 (bf16) or 32 (e4m3) positions
+ * that one block takes of a sequence.
  * The result does not depend on where the pages lie, and repeated calls on the
  * same GPU return the same bits.
  */
